@@ -32,12 +32,11 @@
 // waits (with a fixed bound) for the copies it issued, the MMA issuer waits
 // for a final commit that covers all its MMAs, and only then is TMEM freed;
 // the output tile is left unspecified.
-#include <cuda.h>
-
 #include <algorithm>
 #include <cstring>
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace bv {
 namespace {
@@ -55,7 +54,6 @@ constexpr int W_TILE = MAX_NT * BK * 4;  // 16 KB: one weight operand tile (at m
 constexpr int THREADS = 256;
 constexpr int CONV_WARP0 = 4;            // warps 4..7 convert, add runs, write out
 constexpr int NCONV = 128;
-constexpr long long DRAIN_LIMIT = 1ll << 22;  // polls for in-flight copies when unwinding
 constexpr int TMEM_COLS = 256;           // two accumulators of up to 128 columns
 constexpr int RUN = 4;                   // chunks accumulated in TMEM before an FP32 add
 constexpr int MAX_K = 32;                // largest kernel size (offset table rows)
@@ -83,100 +81,6 @@ constexpr int SMEM_USED = OFF_BAR + 16 * 8;
 constexpr int SMEM_BYTES = SMEM_USED + 1024;             // room to align the base
 static_assert(SMEM_BYTES + 4 * 1024 + 1024 <= 227 * 1024, "shared memory budget");
 
-__device__ __forceinline__ unsigned smem_u32(const void *p) {
-  return (unsigned)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ void mbar_init(unsigned bar, unsigned count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(unsigned bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_tx(unsigned bar, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(unsigned bar, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Non-blocking probe of an mbarrier phase: cheaper than try_wait when the
-// phase has already completed (measured on B200: ~160 against ~280 cycles in
-// the MMA issuer's wait for a weight chunk that had landed long before).
-__device__ __forceinline__ bool mbar_test(unsigned bar, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-struct Ctl {
-  int abort;      // a bounded wait gave up somewhere in the CTA (or its pair)
-  unsigned tmem;  // TMEM base address from tcgen05.alloc
-};
-
-// How a CTA reports a wait that ran out: its own Ctl, the shared::cluster
-// address of its pair peer's abort flag (0 for a lone CTA), the device status
-// word and the poll limit.
-struct WaitCtx {
-  volatile Ctl *ctl;
-  unsigned peer_abort;
-  int *status;
-  long long limit;
-};
-
-__device__ __forceinline__ void raise_abort(const WaitCtx &w, int code) {
-  w.ctl->abort = 1;
-  if (w.peer_abort)
-    asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(w.peer_abort), "r"(1) : "memory");
-  if (w.status) atomicExch(w.status, code);
-}
-
-// Bounded wait on an mbarrier phase: true once the phase has completed;
-// false after w.limit polls (the CTA and its peer are then marked aborted and
-// the failure recorded in the device status word) or once an abort raised
-// elsewhere in the pair is seen.  A role stops issuing work at its first
-// false.
-__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, const WaitCtx &w,
-                                          int code) {
-  if (mbar_test(bar, parity)) return true;
-  for (long long it = 0; it < w.limit; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255) == 255 && w.ctl->abort) return false;
-  }
-  raise_abort(w, code);
-  return false;
-}
-
-// Wait with a fixed bound that does not return early on abort: used to let
-// the copies and MMAs a role issued finish before the CTA frees TMEM or exits.
-__device__ __forceinline__ void mbar_drain(unsigned bar, unsigned parity) {
-  for (long long it = 0; it < DRAIN_LIMIT; ++it)
-    if (mbar_try_wait(bar, parity)) return;
-}
-
-// Converter-side wait: lane 0 polls the barrier, the warp follows it, so the
-// polling does not compete with the conversion for shared-memory bandwidth;
-// the outcome is the same for every lane.
-__device__ __forceinline__ bool warp_wait(unsigned bar, unsigned parity, const WaitCtx &w,
-                                          int code) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, w, code) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
 __device__ __forceinline__ void cp_async4_zfill(float *dst, const float *src, bool valid) {
   const unsigned d = smem_u32(dst);
   const int n = valid ? 4 : 0;
@@ -193,13 +97,6 @@ __device__ __forceinline__ void conv_bar_sync() {  // the four converter warps
   asm volatile("bar.sync 1, %0;\n" ::"n"(NCONV) : "memory");
 }
 
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart (stride byte offset), descriptor version 1.
-__device__ __forceinline__ uint64_t sw128_desc(unsigned addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
 // Instruction descriptor: D f32, A and B tf32, both K-major, M = 128, N = nt.
 __host__ __device__ constexpr uint32_t make_idesc(int nt) {
   return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(nt >> 3) << 17) |
@@ -214,12 +111,6 @@ __device__ __forceinline__ void mma_tf32(unsigned tmem_d, uint64_t a, uint64_t b
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit(unsigned bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
-      : "memory");
-}
-
 // Byte offset of element (row r, column k < 32) in a K-major SW128 tile of
 // 128-byte rows: 8-row groups of 1024 bytes, 16-byte chunk index XOR (r % 8).
 __device__ __forceinline__ int sw128_off(int r, int k) {
@@ -554,30 +445,6 @@ conv1d_tc_kernel(const __grid_constant__ CUtensorMap tmap_w,
   }
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no
-// link-time dependency on libcuda).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-    else
-      cudaGetLastError();
-  }
-  return fn;
-}
-
 // Channels per CTA: split Cout into the fewest tiles of at most 128 and round
 // each to a multiple of 16 (the UMMA N granularity for M = 128).
 int pick_nt(int Cout) {
@@ -722,21 +589,6 @@ __host__ __device__ constexpr uint32_t make_idesc_pair_f16(int nt) {
   return (1u << 4) | ((uint32_t)(nt >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
 }
 
-__device__ __forceinline__ unsigned cluster_rank() {
-  unsigned r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
-                   : "memory");
-}
-// Shared::cluster address of the same variable in CTA `rank` of the cluster.
-__device__ __forceinline__ unsigned map_to_rank(unsigned addr, unsigned rank) {
-  unsigned r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 // Relaxed: the arrive publishes no data of this thread's.  Its one use says
 // that this thread's TMEM reads of a run accumulator are complete
 // (tcgen05.wait::ld returned their values, then tcgen05.fence::before_thread_sync),
@@ -747,23 +599,12 @@ __device__ __forceinline__ void mbar_arrive_remote(unsigned cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr)
                : "memory");
 }
-// TMA loads of the pair: the destination is this CTA's shared memory, the
-// completion goes to the even CTA's barrier (peer bit cleared).
-constexpr unsigned kPeerBitMask = 0xFEFFFFFFu;
 __device__ __forceinline__ void tma_load_3d_pair(unsigned dst, const CUtensorMap *map, int c0, int c1,
                                                  int c2, unsigned bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar & kPeerBitMask)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_pair(unsigned dst, const CUtensorMap *map, int c0, int c1,
-                                                 unsigned bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar & kPeerBitMask)
       : "memory");
 }
 // The A-collector qualifier: FILL keeps this MMA's A operand in the
@@ -791,16 +632,6 @@ __device__ __forceinline__ void mma_split_pair(unsigned tmem_d, uint64_t a, uint
   }
 }
 #undef BV_MMA_PAIR
-// Arrive on the barrier at this offset in both CTAs once the MMAs issued so
-// far have completed.
-__device__ __forceinline__ void mma_commit_pair(unsigned bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n" ::"r"(bar),
-      "h"((unsigned short)3)
-      : "memory");
-}
-
 // Bulk-tensor store of a staged box (this CTA's shared memory -> global),
 // tracked per thread in bulk groups.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, unsigned src, int c0, int c1,
