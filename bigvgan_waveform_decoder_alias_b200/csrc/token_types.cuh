@@ -1,0 +1,87 @@
+// Element types, row views and argument checks shared by the token operators.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace bv {
+
+inline bool dtype_ok(int dt) { return dt == BV_F32 || dt == BV_BF16 || dt == BV_F16; }
+inline int dtype_size(int dt) { return dt == BV_F32 ? 4 : 2; }
+
+// `rows` rows of `row_bytes` bytes, `stride` bytes apart.
+struct RowView {
+  const void *p;
+  int64_t rows, stride, row_bytes;
+};
+
+// Do two views share a byte?  Views of one stride are compared within the
+// stride (column slices of one matrix are disjoint); others by their spans.
+inline bool rows_overlap(const RowView &a, const RowView &b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1) return false;
+  const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a.p);
+  const int64_t pb = (int64_t)reinterpret_cast<uintptr_t>(b.p);
+  const int64_t ea = pa + (a.rows - 1) * a.stride + a.row_bytes;
+  const int64_t eb = pb + (b.rows - 1) * b.stride + b.row_bytes;
+  if (ea <= pb || eb <= pa) return false;
+  if (a.stride == b.stride && a.rows > 1 && b.rows > 1 && a.row_bytes <= a.stride &&
+      b.row_bytes <= b.stride) {
+    const int64_t d = ((pb - pa) % a.stride + a.stride) % a.stride;  // b's rows start d into a's
+    return !(d >= a.row_bytes && d + b.row_bytes <= a.stride);
+  }
+  return true;
+}
+inline bool same_rows(const RowView &a, const RowView &b) {
+  return a.p == b.p && (a.stride == b.stride || a.rows <= 1);
+}
+
+inline bool aligned_to(const void *p, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+
+// ---- launchers (arguments checked by the ABI entries) ------------------------
+
+struct NormArgs {
+  const void *x, *residual, *gain;  // residual, gain may be null
+  void *sum, *y;                    // may be null
+  int8_t *q;                        // may be null
+  float *scale;
+  int64_t xs, rs, ss, ys, qs;  // strides in elements
+  int64_t rows;
+  int cols;
+  float eps;
+  int norm;  // 0: rows are quantised as they are (no norm, residual or gain)
+};
+bv_status launch_rows(const NormArgs &a, int dtype, int gain_dtype, cudaStream_t st);
+
+struct Int8Args {
+  const int8_t *a, *w;
+  const float *a_scale, *w_scale, *bias;  // bias may be null
+  const void *residual;                   // may be null; may be y
+  void *y;
+  int64_t as, ws, rs, ys;  // strides: bytes, bytes, elements, elements
+  int M, N, K;
+  int channels_first;
+};
+bv_status launch_int8_matmul(const Int8Args &a, int dtype, cudaStream_t st);
+
+}  // namespace bv

@@ -7,6 +7,7 @@ fallback: if libbv.so cannot be loaded, or a call fails, a BVError is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -204,6 +205,18 @@ def lib():
     L.bv_decode_host_workspace_size.argtypes = [ctypes.POINTER(DecoderConfig), c_int, c_int]
     L.bv_decode_host.argtypes = [ctypes.POINTER(DecoderConfig), ctypes.POINTER(DecoderWeights),
                                  _fp, c_int, c_int, _fp, _fp, c_size, _fp]
+    c_i64 = ctypes.c_int64
+    norm = [_fp, c_i64, _fp, c_i64, _fp, c_i64, _fp, c_int, c_float, c_i64, c_int, c_int, _fp, c_i64]
+    L.bv_rms_norm.argtypes = norm + [_fp]
+    L.bv_rms_norm_int8.argtypes = norm + [_fp, _fp]
+    L.bv_quantize_rows.argtypes = [_fp, c_i64, c_i64, c_int, c_int, _fp, c_i64, _fp, _fp]
+    L.bv_int8_matmul.argtypes = [_fp, c_i64, _fp, _fp, c_i64, _fp, _fp, c_int, c_int, c_int, _fp,
+                                 c_i64, _fp, c_i64, c_int, c_int, _fp]
+    L.bv_token_front_end_workspace_size.restype = c_size
+    L.bv_token_front_end_workspace_size.argtypes = [c_int] * 3
+    L.bv_token_front_end.argtypes = [_fp, c_i64, _fp, c_i64, _fp, c_int, c_float, c_int, c_int,
+                                     c_int, c_int, _fp, c_i64, _fp, _fp, c_int, c_int, _fp, _fp,
+                                     c_size, _fp]
     _LIB = L
     return L
 
@@ -534,6 +547,15 @@ class Decoder:
                                _ptr(y), _ptr(ws), ws.numel() * 4, _stream(stream)))
         return y
 
+    def decode_tokens(self, x: torch.Tensor, front: "TokenFrontEnd", residual=None, y=None,
+                      workspace=None, stream=None) -> torch.Tensor:
+        """Hidden states x [B, frames, cols] of a model -> waveform: the token
+        front end into this decoder's latents, then decode().  `workspace`
+        is the decode's; the front end takes its own."""
+        with _On(stream, x):
+            z = front(x, residual, by_side=self.cfg.latent_channels == 0)
+            return self.decode(z, y, workspace)
+
     # ------------------------------------------------ units, for sharding
     def tile_count(self, frames: int) -> int:
         return int(lib().bv_decoder_tile_count(ctypes.byref(self.cfg), frames))
@@ -692,3 +714,220 @@ class BweTail:
                                  _ptr(self.mel_basis), sp.n_mels, sp.ratio, _ptr(y),
                                  _ptr(workspace), workspace.numel() * 4, _stream(stream)))
         return y
+
+
+# --------------------------------------------------------- token operators
+
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(pointer, stride, rows, cols) of t seen as [rows, cols]: consecutive
+    elements within a row, one stride between rows."""
+    if not t.is_cuda:
+        raise BVError(1, f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        if t.dim() == 0:
+            raise BVError(2, f"{name} needs a last dimension")
+        try:
+            t = t.view(math.prod(t.shape[:-1]), t.shape[-1])
+        except RuntimeError:
+            raise BVError(1, f"{name} has no single stride between its rows") from None
+    rows, cols = t.shape
+    stride, one = t.stride()
+    if one != 1 and cols > 1:
+        raise BVError(1, f"the rows of {name} must be contiguous")
+    return t.data_ptr(), (stride if rows > 1 else cols), rows, cols
+
+
+def _vec(t: Optional[torch.Tensor], n: int, name: str, dtype=torch.float32):
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise BVError(1, f"{name} must be a contiguous {dtype} CUDA tensor of {n} values")
+    return t.data_ptr()
+
+
+class _On:
+    """The device and stream of a call: the tensors' device is made current,
+    and new outputs belong to the stream that writes them."""
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].device
+        if dev.type != "cuda":
+            raise BVError(1, "tensors must be CUDA tensors")
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise BVError(1, f"tensors on {dev} and {t.device}")
+        self.ctx = []
+        if dev.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(dev))
+        if stream is not None:
+            if stream.device != dev:
+                raise BVError(1, f"tensors on {dev}, the stream on {stream.device}")
+            self.ctx.append(torch.cuda.stream(stream))
+        self.index = dev.index
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _int8_rows(shape, device) -> torch.Tensor:
+    """int8 [..., cols] whose rows start on 16 bytes, as bv_int8_matmul reads
+    them fastest: cols of each padded row (the padding holds nothing)."""
+    cols = shape[-1]
+    return torch.empty((*shape[:-1], (cols + 15) // 16 * 16), device=device,
+                       dtype=torch.int8)[..., :cols]
+
+
+def _like(t, x, dtype, name):
+    if t.shape != x.shape or t.dtype != dtype:
+        raise BVError(2, f"{name} must be {dtype} of shape {tuple(x.shape)}")
+    return t
+
+
+def _norm_args(x, gain, residual, h):
+    if x.dtype not in DTYPES:
+        raise BVError(1, f"x of type {x.dtype}")
+    xp, xs, rows, cols = _rows(x, "x")
+    rp = hp = gp = None
+    rs = hs = 0
+    if residual is not None:
+        rp, rs, _, _ = _rows(_like(residual, x, x.dtype, "residual"), "residual")
+    if h is not None:
+        hp, hs, _, _ = _rows(_like(h, x, x.dtype, "h"), "h")
+    gdt = 0
+    if gain is not None:
+        if gain.dtype not in DTYPES:
+            raise BVError(1, f"gain of type {gain.dtype}")
+        gdt = DTYPES[gain.dtype]
+        gp = _vec(gain, cols, "gain", gain.dtype)
+    return xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, DTYPES[x.dtype]
+
+
+def bv_rms_norm(x, gain=None, eps=1e-6, residual=None, h=None, y=None, stream=None):
+    """Root-mean-square norm of the rows of x [..., cols] (+ residual) times
+    gain [cols].  Returns y, with a residual (y, h), h = x + residual in x's
+    type; h may be given, and may be x or the residual itself."""
+    with _On(stream, x, gain, residual, h, y) as st:
+        if residual is not None and h is None:
+            h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
+        yp, ys, _, _ = _rows(_like(y, x, x.dtype, "y"), "y")
+        _check(lib().bv_rms_norm(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, yp, ys, st))
+    return y if residual is None else (y, h)
+
+
+def bv_rms_norm_int8(x, gain=None, eps=1e-6, residual=None, h=None, q=None, scale=None,
+                     stream=None):
+    """bv_rms_norm with 8-bit rows: (q int8 [..., cols], scale f32 [...]) with
+    y = q scale, and h as a third with a residual."""
+    with _On(stream, x, gain, residual, h, q, scale) as st:
+        if residual is not None and h is None:
+            h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h)
+        q = _int8_rows(x.shape, x.device) if q is None else q
+        qp, qs, _, _ = _rows(_like(q, x, torch.int8, "q"), "q")
+        scale = torch.empty(x.shape[:-1], device=x.device) if scale is None else scale
+        _check(lib().bv_rms_norm_int8(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, qp, qs,
+                                      _vec(scale, rows, "scale"), st))
+    return (q, scale) if residual is None else (q, scale, h)
+
+
+def bv_quantize_rows(x, q=None, scale=None, stream=None):
+    """The rows of x [..., cols] in 8 bits: (q int8 [..., cols], scale f32
+    [...]); tokens [M, K] or a weight [N, K] for bv_int8_matmul."""
+    if x.dtype not in DTYPES:
+        raise BVError(1, f"x of type {x.dtype}")
+    with _On(stream, x, q, scale) as st:
+        xp, xs, rows, cols = _rows(x, "x")
+        q = _int8_rows(x.shape, x.device) if q is None else q
+        qp, qs, _, _ = _rows(_like(q, x, torch.int8, "q"), "q")
+        scale = torch.empty(x.shape[:-1], device=x.device) if scale is None else scale
+        _check(lib().bv_quantize_rows(xp, xs, rows, cols, DTYPES[x.dtype], qp, qs,
+                                      _vec(scale, rows, "scale"), st))
+    return q, scale
+
+
+def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=None,
+                   channels_first=False, y=None, stream=None):
+    """a int8 [..., K] (scales a_scale [...]) times w int8 [N, K] (w_scale
+    [N]): y [..., N], or with channels_first [N, tokens].  out_dtype: f32 (the
+    default), bf16 or f16; y's or the residual's where one is given."""
+    if a.dtype != torch.int8 or w.dtype != torch.int8:
+        raise BVError(1, "a and w must be int8")
+    with _On(stream, a, a_scale, w, w_scale, bias, residual, y) as st:
+        ap, as_, M, K = _rows(a, "a")
+        wp, ws, N, Kw = _rows(w, "w")
+        if w.dim() != 2 or K != Kw:
+            raise BVError(2, f"a [..., {K}] times w {tuple(w.shape)}")
+        if out_dtype is None:
+            out_dtype = (y if y is not None else residual).dtype \
+                if y is not None or residual is not None else torch.float32
+        if out_dtype not in DTYPES:
+            raise BVError(1, f"y of type {out_dtype}")
+        shape = (N, M) if channels_first else (*a.shape[:-1], N)
+        y = torch.empty(shape, device=a.device, dtype=out_dtype) if y is None else y
+        if tuple(y.shape) != shape or y.dtype != out_dtype:
+            raise BVError(2, f"y must be {out_dtype} of shape {shape}")
+        yp, ys, _, _ = _rows(y, "y")
+        rp, rs = None, 0
+        if residual is not None:
+            rp, rs, _, _ = _rows(_like(residual, y, out_dtype, "residual"), "residual")
+        _check(lib().bv_int8_matmul(ap, as_, _vec(a_scale, M, "a_scale"), wp, ws,
+                                    _vec(w_scale, N, "w_scale"), _vec(bias, N, "bias"), M, N, K,
+                                    rp, rs, yp, ys, DTYPES[out_dtype], int(bool(channels_first)),
+                                    st))
+    return y
+
+
+class TokenFrontEnd:
+    """A model's last norm and its projection into latents, in 8 bits: gain
+    [cols] or None, weight [Cout, cols] (quantised here, one scale a channel),
+    bias [Cout] or None."""
+
+    def __init__(self, gain, weight, bias=None, eps=1e-6, device="cuda"):
+        weight = torch.as_tensor(weight).to(device)
+        if weight.dim() != 2:
+            raise BVError(2, f"weight of shape {tuple(weight.shape)}")
+        self.w, self.w_scale = bv_quantize_rows(weight)
+        self.gain = None if gain is None else torch.as_tensor(gain).to(device).contiguous()
+        self.bias = None if bias is None else \
+            torch.as_tensor(bias, dtype=torch.float32).to(device).contiguous()
+        self.eps = eps
+
+    def __call__(self, x, residual=None, by_side=False, z=None, workspace=None, stream=None):
+        """x [S, T, cols] (+ residual) -> latents [Cout, S, T], or [S, Cout, T]
+        with by_side."""
+        if x.dim() != 3:
+            raise BVError(2, f"x of shape {tuple(x.shape)}")
+        S, T, D = x.shape
+        Cout = self.w.shape[0]
+        if D != self.w.shape[1]:
+            raise BVError(2, f"x [..., {D}], weight {tuple(self.w.shape)}")
+        with _On(stream, x, residual, self.gain, self.w, self.bias, z, workspace) as st:
+            xp, xs, rp, rs, _, _, gp, gdt, rows, cols, dt = _norm_args(x, self.gain, residual, None)
+            shape = (S, Cout, T) if by_side else (Cout, S, T)
+            if z is None:
+                z = torch.empty(shape, device=x.device, dtype=torch.float32)
+            elif tuple(z.shape) != shape:
+                raise BVError(2, f"z must have shape {shape}")
+            need = int(lib().bv_token_front_end_workspace_size(S, T, D))
+            if need == 0:
+                raise BVError(2, last_error())
+            if workspace is None:
+                workspace = torch.empty(need // 4 + 64, device=x.device, dtype=torch.float32)
+            _check(lib().bv_token_front_end(xp, xs, rp, rs, gp, gdt, self.eps, S, T, D, dt,
+                                            self.w.data_ptr(), self.w.stride(0),
+                                            _vec(self.w_scale, Cout, "w_scale"),
+                                            _vec(self.bias, Cout, "bias"), Cout,
+                                            int(bool(by_side)), _ptr(z), _ptr(workspace),
+                                            workspace.numel() * 4, st))
+        return z

@@ -598,6 +598,96 @@ bv_status bv_decode_host(const bv_decoder_config *cfg,
                          int B, int frames, float *y_host, void *workspace,
                          size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Token operators: the last layers of a generative model in front of a
+ * decoder, served in 8 bits.  Their tensors are rows [rows, cols] with
+ * consecutive elements and a stride between rows, counted in elements (the
+ * general convention of contiguous float32 [B, C, T] does not hold here);
+ * element types are bv_dtype.  Strides of inputs may be anything from 0 up
+ * (0 reads one row for all); rows of outputs must not overlap.  Bytes between
+ * the rows of an output are left as they were.  rows = 0 (M = 0) is a valid
+ * empty call.  Pointers need their element's alignment only.
+ * All are inference operators: the library has no backward passes.
+ * ---------------------------------------------------------------------- */
+typedef enum { BV_F32 = 0, BV_BF16 = 1, BV_F16 = 2 } bv_dtype;
+
+/* Root-mean-square norm with the residual's addition.  Per row, in 32 bits:
+ *   h = x + residual (residual NULL: h = x);   sum = h rounded to dtype;
+ *   y = h gain / sqrt(mean(h^2) + eps)         (gain NULL: ones)
+ * The norm reads h before its rounding.  x, residual, sum and y have type
+ * `dtype`; gain [cols] has type gain_dtype, BV_F32 or dtype.  sum may be NULL
+ * and may be x or the residual (same pointer and stride); every other overlap
+ * of an output is refused.  A row whose h^2 overflows 32 bits is summed
+ * scaled; NaN and infinities in a row show in that row alone.
+ * bv_rms_norm_int8 writes 8-bit rows and a scale for each row instead of y:
+ *   t = h gain, a = max |t|, q = rint(t (127 / a)) in [-127, 127],
+ *   scale = a / (127 sqrt(mean(h^2) + eps)),
+ * so y is q scale to half a step.  q is the same for any batch and any
+ * launch shape.  A row of zeros has q = 0, scale = 0; a row in which some t
+ * is not finite has q = 0, scale = NaN (its products are NaN).
+ * Errors: BV_ERR_ARG (null, misaligned or overlapping pointer, bad type,
+ * eps not in (0, 1e30)), BV_ERR_SHAPE (rows < 0, cols < 1, strides). */
+bv_status bv_rms_norm(const void *x, int64_t x_stride, const void *residual,
+                      int64_t residual_stride, void *sum, int64_t sum_stride,
+                      const void *gain, int gain_dtype, float eps,
+                      int64_t rows, int cols, int dtype, void *y,
+                      int64_t y_stride, void *stream);
+bv_status bv_rms_norm_int8(const void *x, int64_t x_stride,
+                           const void *residual, int64_t residual_stride,
+                           void *sum, int64_t sum_stride, const void *gain,
+                           int gain_dtype, float eps, int64_t rows, int cols,
+                           int dtype, int8_t *q, int64_t q_stride,
+                           float *scale, void *stream);
+
+/* Rows in 8 bits with a scale for each row, as above with t = x and
+ * scale = a / 127: the operands of bv_int8_matmul where no norm writes them
+ * (tokens [M, K]; a weight [N, K], one scale for each output channel). */
+bv_status bv_quantize_rows(const void *x, int64_t x_stride, int64_t rows,
+                           int cols, int dtype, int8_t *q, int64_t q_stride,
+                           float *scale, void *stream);
+
+/* Matrix product of 8-bit integers with scales for each token and channel:
+ *   y[m, n] = a_scale[m] w_scale[n] sum_k a[m, k] w[n, k] + bias[n]
+ *             + residual[m, n],
+ * the sum exact in 32-bit integers, the rest in 32-bit floats, rounded once
+ * to dtype.  a [M, K] with row stride a_stride, w [N, K] with w_stride (in
+ * bytes; any values in [-128, 127]); a_scale [M], w_scale [N], bias [N] or
+ * NULL: f32.  y and residual (or NULL; it may be y itself) have type dtype:
+ * [M, N], or with channels_first [N, M] (tokens fastest: the latents
+ * bv_decode reads).  K up to BV_INT8_MAX_DEPTH.  Rows of a and w that start
+ * on 16 bytes (aligned pointer, stride a multiple of 16) are read fastest.
+ * Errors: BV_ERR_ARG (null, misaligned or overlapping pointer, bad type),
+ * BV_ERR_SHAPE (M < 0, N < 1, K out of range, strides). */
+#define BV_INT8_MAX_DEPTH 131071
+bv_status bv_int8_matmul(const int8_t *a, int64_t a_stride,
+                         const float *a_scale, const int8_t *w,
+                         int64_t w_stride, const float *w_scale,
+                         const float *bias, int M, int N, int K,
+                         const void *residual, int64_t residual_stride,
+                         void *y, int64_t y_stride, int dtype,
+                         int channels_first, void *stream);
+
+/* The token front end: a model's last norm and its projection to latents,
+ *   z = w_scale (w q^T) scale + bias,  (q, scale) = bv_rms_norm_int8(x, ...),
+ * for S sides of T frames, token (s, t) at row s T + t of x (and residual)
+ * [S T, cols].  z (f32) is laid out as the decoders read it: [Cout, S, T], the
+ * normalised latents of bv_latent_front_end and of bv_decode with
+ * latent_channels = Cout; or with by_side [S, Cout, T], the input of
+ * bv_decode without its front end and of bv_dav_decode.  w [Cout, cols],
+ * w_scale, bias as in bv_int8_matmul.  The workspace (256-byte aligned) is
+ * disjoint from every tensor and belongs to the call until it has run: two
+ * calls that may run at once need two.
+ * Errors: as the two operators, and BV_ERR_WORKSPACE. */
+size_t bv_token_front_end_workspace_size(int S, int T, int cols);
+bv_status bv_token_front_end(const void *x, int64_t x_stride,
+                             const void *residual, int64_t residual_stride,
+                             const void *gain, int gain_dtype, float eps,
+                             int S, int T, int cols, int dtype,
+                             const int8_t *w, int64_t w_stride,
+                             const float *w_scale, const float *bias, int Cout,
+                             int by_side, float *z, void *workspace,
+                             size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
