@@ -3,74 +3,476 @@
 // The sum is exact in 32-bit integers (|a w| <= 2^14 and K < 2^17), so it does
 // not depend on how K is split; the scales, the bias and the residual join in
 // 32-bit floats and the result is rounded once.
+//
+// Both kernels see the product as rows x columns, the rows being the
+// dimension that y keeps consecutive: channels, or tokens where y is channels
+// first.  Rows are the tensor core's M side, so a TMEM lane is one row and a
+// warp writes 32 consecutive outputs of a column.  Operand tiles are K-major,
+// 128 bytes (128 values) a row, 128-byte swizzle.
+#include <algorithm>
+
+#include "tc_ptx.cuh"
 #include "token_types.cuh"
 
 namespace bv {
 namespace {
 
-constexpr int TILE = 64, KC = 32;
+constexpr int BR = 128;       // rows of a CTA's tile
+constexpr int BK = 128;       // values of K in a stage: one swizzled row
+constexpr int MAX_SPLIT = 8;  // CTAs of a cluster that share a tile's K
 
-// 64 x 64 outputs a block, 4 x 4 a thread, four products an instruction; the
-// operands are read byte by byte, so rows may start anywhere.
-template <typename T>
-__global__ void __launch_bounds__(256) int8_tile_kernel(Int8Args p, int tiles_m) {
-  __shared__ int as[KC / 4][TILE + 1], ws[KC / 4][TILE + 1];
-  const int m0 = (int)(blockIdx.x % tiles_m) * TILE, n0 = (int)(blockIdx.x / tiles_m) * TILE;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += KC) {
-    for (int i = threadIdx.x; i < TILE * (KC / 4); i += 256) {
-      const int k4 = i % (KC / 4), r = i / (KC / 4);
-      unsigned va = 0, vw = 0;
-      for (int b = 0; b < 4; ++b) {
-        const int k = k0 + 4 * k4 + b;
-        if (k < p.K) {
-          if (m0 + r < p.M) va |= (unsigned)(uint8_t)p.a[(int64_t)(m0 + r) * p.as + k] << (8 * b);
-          if (n0 + r < p.N) vw |= (unsigned)(uint8_t)p.w[(int64_t)(n0 + r) * p.ws + k] << (8 * b);
+// The product as rows x columns; element (row, col) of y at col ys + row.
+struct Mm {
+  const int8_t *r, *c;  // [rows, K], [cols, K]
+  int64_t rstride, cstride;
+  int rows, cols, K;
+  const float *r_scale, *c_scale;
+  const float *r_bias, *c_bias;  // one of them, or none
+  const void *residual;          // may be y
+  void *y;
+  int64_t rs, ys;
+  bool pairs;  // 16-bit outputs: y takes two rows in one aligned store
+};
+
+// Instruction descriptor of kind::i8: D s32, A and B s8, both K-major.
+__host__ __device__ constexpr uint32_t i8_idesc(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
+template <int CTAS>
+__device__ __forceinline__ void mma_i8(unsigned tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       unsigned acc) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(unsigned dst, const CUtensorMap *map, int c0, int c1,
+                                            unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+// 16 accumulator columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(unsigned addr, int *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
+      "%12,%13,%14,%15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+
+__device__ __forceinline__ unsigned bits16(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+__device__ __forceinline__ unsigned bits16(__half v) { return __half_as_ushort(v); }
+__device__ __forceinline__ unsigned bits16(float) { return 0; }
+
+// A warp's 32 rows (row0 + lane) x N columns from col0 of the accumulator go
+// out: `rscale`, `rbias` are this lane's row's.  The residual's loads are
+// issued before the first store (it may be y: each element is read by the
+// thread that writes it, in this call).  A 16-bit column is half a word a
+// lane, so lanes swap halves in pairs: the even one writes two rows of the
+// even column, the odd one two rows of the odd column.
+template <typename T, int N>
+__device__ __forceinline__ void store_columns(const Mm &p, const int (&acc)[N], int row0, int lane,
+                                              int col0, float rscale, float rbias) {
+  static_assert(N <= 32 && N % 2 == 0, "one column's scale a lane");
+  const int row = row0 + lane;
+  const int nc = min(N, p.cols - col0);  // warp-uniform
+  if (row0 >= p.rows || nc <= 0) return;
+  const bool in = row < p.rows;
+  const bool mine = lane < nc;
+  const float cs = mine ? __ldg(p.c_scale + col0 + lane) : 0.0f;
+  const float cb = mine && p.c_bias ? __ldg(p.c_bias + col0 + lane) : 0.0f;
+  T *y = static_cast<T *>(p.y) + (int64_t)col0 * p.ys + row;
+  const T *res = static_cast<const T *>(p.residual) + (int64_t)col0 * p.rs + row;
+  T r[N];
+  if (p.residual) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (in && e < nc) r[e] = res[e * p.rs];
+  }
+  const bool pairs = sizeof(T) == 2 && p.pairs && row0 + 32 <= p.rows;
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    T v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float s = rscale * __shfl_sync(0xffffffffu, cs, e + j);
+      float f = fmaf((float)acc[e + j], s, rbias + __shfl_sync(0xffffffffu, cb, e + j));
+      if (p.residual && in && e + j < nc) f += to_f32(r[e + j]);
+      v[j] = from_f32<T>(f);
+    }
+    if (pairs) {
+      const int odd = lane & 1;
+      const unsigned got = __shfl_xor_sync(0xffffffffu, odd ? bits16(v[0]) : bits16(v[1]), 1);
+      const unsigned word = odd ? (got | (bits16(v[1]) << 16)) : (bits16(v[0]) | (got << 16));
+      if (e + odd < nc) *reinterpret_cast<unsigned *>(y + (e + odd) * p.ys - odd) = word;
+    } else if (in) {
+      if (e < nc) y[e * p.ys] = v[0];
+      if (e + 1 < nc) y[(e + 1) * p.ys] = v[1];
+    }
+  }
+}
+
+__host__ __device__ constexpr int tmem_cols(int n) {
+  return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512;
+}
+
+// ------------------------------------------------------- few columns or tiles
+//
+// One CTA a tile of 128 rows x NT columns, or a cluster of up to eight CTAs
+// that take a share of K each: with few tokens the weight's bytes bound the
+// product, and only a split over K gives every SM some of them.  The shares
+// are joined through distributed shared memory: each CTA leaves its partial
+// sums in its own, then sums and writes the columns col % split = rank.
+// Integers, so the join's order does not show.
+//
+// TMA: thread 0 loads the stages by TMA.  Otherwise (rows that do not start on
+// 16 bytes) warps 4..7 copy them: aligned words, shifted into place.
+
+constexpr int TILE_MAX_STAGES = 12;
+
+template <int NT>
+constexpr int tile_stage_bytes() {
+  return (BR + NT) * BK;
+}
+
+// 16 bytes of K from byte k on of a row, zero past K.  Aligned words are
+// read where the whole word lies inside the operand [lo, hi), else bytes.
+__device__ __forceinline__ uint4 load16(const int8_t *row, int k, int K, const int8_t *lo,
+                                        const int8_t *hi) {
+  uint4 out = make_uint4(0, 0, 0, 0);
+  const int nb = min(16, K - k);
+  if (nb <= 0) return out;
+  const int8_t *p = row + k;
+  const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+  const int8_t *a = p - sh;
+  unsigned w[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    w[i] = 0;
+    const int8_t *q = a + 4 * i;
+    if (q < p + nb) {
+      if (q >= lo && q + 4 <= hi) {
+        w[i] = __ldg(reinterpret_cast<const unsigned *>(q));
+      } else {
+        for (int b = 0; b < 4; ++b)
+          if (q + b >= lo && q + b < hi) w[i] |= (unsigned)(uint8_t)__ldg(q + b) << (8 * b);
+      }
+    }
+  }
+  unsigned v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __funnelshift_r(w[i], w[i + 1], 8 * sh);
+    const int left = nb - 4 * i;  // bytes of this word inside K
+    if (left < 4) v[i] = left <= 0 ? 0u : v[i] & (0xffffffffu >> (32 - 8 * left));
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <typename T, int NT, bool TMA>
+__global__ void __launch_bounds__(TMA ? 128 : 256)
+int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_c,
+                 const Mm p, int tiles_r, int split, int stages, int *status,
+                 long long wait_limit) {
+  constexpr int STAGE = tile_stage_bytes<NT>();
+  constexpr unsigned TMEM = tmem_cols(NT);
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t bars[2 * TILE_MAX_STAGES + 1];
+  __shared__ Ctl ctl;
+  const unsigned bar_full = smem_u32(&bars[0]);
+  const unsigned bar_empty = smem_u32(&bars[TILE_MAX_STAGES]);
+  const unsigned bar_done = smem_u32(&bars[2 * TILE_MAX_STAGES]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)(blockIdx.x % (unsigned)split), tile = (int)(blockIdx.x / (unsigned)split);
+  const int row0 = tile % tiles_r * BR, col0 = tile / tiles_r * NT;
+  const int chunks = (p.K + BK - 1) / BK;
+  const int c0 = (int)((int64_t)chunks * rank / split);
+  const int n = (int)((int64_t)chunks * (rank + 1) / split) - c0;
+  const WaitCtx wc{&ctl, 0u, status, wait_limit};
+
+  if (threadIdx.x == 0) {
+    ctl.abort = 0;
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(bar_full + 8 * s, TMA ? 1 : 4);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    mbar_init(bar_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+                     smem_u32(&ctl.tmem)),
+                 "n"(TMEM)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+  const unsigned tmem = ctl.tmem;
+
+  if (TMA && warp == 0 && lane == 0) {
+    int c = 0;
+    for (; c < n; ++c) {
+      const int s = c % stages, u = c / stages;
+      if (u > 0 && !mbar_wait(bar_empty + 8 * s, (u - 1) & 1, wc, 301)) break;
+      const unsigned dst = smem_u32(smem + s * STAGE), fb = bar_full + 8 * s;
+      mbar_arrive_tx(fb, STAGE);
+      tma_load_2d(dst, &map_r, (c0 + c) * BK, row0, fb);
+      tma_load_2d(dst + BR * BK, &map_c, (c0 + c) * BK, col0, fb);
+    }
+    // the last load into each slot has landed before the CTA can exit
+    for (int d = c - stages; d < c; ++d)
+      if (d >= 0) mbar_drain(bar_full + 8 * (d % stages), (d / stages) & 1);
+  } else if (warp == 1 && lane == 0) {
+    for (int c = 0; c < n; ++c) {
+      const int s = c % stages;
+      if (!mbar_wait(bar_full + 8 * s, (c / stages) & 1, wc, 302)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+      const unsigned at = smem_u32(smem + s * STAGE);
+      const uint64_t da = sw128_desc(at), db = sw128_desc(at + BR * BK);
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k)  // 32 values = 32 bytes an MMA
+        mma_i8<1>(tmem, da + 2 * k, db + 2 * k, i8_idesc(BR, NT), c > 0 || k > 0 ? 1u : 0u);
+      mma_commit(bar_empty + 8 * s);
+    }
+    mma_commit(bar_done);
+    mbar_drain(bar_done, 0);  // after an abort too, no MMA outlives the tile
+  } else if (!TMA && warp >= 4) {
+    // each warp's lanes take 4 rows x 8 pieces of 16 bytes at a time
+    const int8_t *rlo = p.r, *rhi = p.r + (int64_t)(p.rows - 1) * p.rstride + p.K;
+    const int8_t *clo = p.c, *chi = p.c + (int64_t)(p.cols - 1) * p.cstride + p.K;
+    const int piece = lane & 7, sub = (warp - 4) * 4 + (lane >> 3);  // 16 rows a pass
+    for (int c = 0; c < n; ++c) {
+      const int s = c % stages, u = c / stages;
+      if (u > 0 && !warp_wait(bar_empty + 8 * s, (u - 1) & 1, wc, 303)) break;
+      unsigned char *at = smem + s * STAGE;
+      const int k = (c0 + c) * BK + 16 * piece;
+#pragma unroll
+      for (int g = 0; g < (BR + NT) / 16; g += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * (g + i) + sub;  // row of the stage: BR rows, then NT columns
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (16 * (g + i) >= BR + NT) continue;
+          if (r < BR) {
+            if (row0 + r < p.rows) v[i] = load16(p.r + (row0 + r) * p.rstride, k, p.K, rlo, rhi);
+          } else if (col0 + r - BR < p.cols) {
+            v[i] = load16(p.c + (col0 + r - BR) * p.cstride, k, p.K, clo, chi);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * (g + i) + sub;
+          if (16 * (g + i) < BR + NT)
+            *reinterpret_cast<uint4 *>(at + r * BK + ((piece ^ (r & 7)) << 4)) = v[i];
         }
       }
-      as[k4][r] = (int)va;
-      ws[k4][r] = (int)vw;
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_full + 8 * s);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < KC / 4; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __dp4a(as[k][ty + 16 * i], ws[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
   }
-  const T *res = static_cast<const T *>(p.residual);
-  T *y = static_cast<T *>(p.y);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= p.M || n >= p.N) continue;
-      float v = (float)acc[i][j] * (p.a_scale[m] * p.w_scale[n]);
-      if (p.bias) v += p.bias[n];
-      const int64_t ri = p.channels_first ? n * p.rs + m : m * p.rs + n;
-      const int64_t yi = p.channels_first ? n * p.ys + m : m * p.ys + n;
-      if (res) v += to_f32(res[ri]);
-      y[yi] = from_f32<T>(v);
+  __syncwarp();
+
+  if (warp < 4) {
+    warp_wait(bar_done, 0, wc, 304);
+    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+  }
+  const unsigned lanes = (unsigned)(32 * warp) << 16;  // of warps 0..3
+  const int row = row0 + 32 * warp + lane;
+  const bool in = warp < 4 && row < p.rows;
+  const float rscale = in ? __ldg(p.r_scale + row) : 0.0f;
+  const float rbias = in && p.r_bias ? __ldg(p.r_bias + row) : 0.0f;
+  if (split == 1) {
+    if (warp < 4) {
+#pragma unroll
+      for (int c = 0; c < NT; c += 16) {
+        int v[16];
+        tmem_ld16(tmem + lanes + c, v);
+        tmem_wait_ld();
+        if (!ctl.abort)
+          store_columns<T, 16>(p, v, row0 + 32 * warp, lane, col0 + c, rscale, rbias);
+      }
     }
+  } else {
+    // partial sums [NT][128] over the stages, which no copy or MMA uses now
+    int *part = reinterpret_cast<int *>(smem);
+    if (warp < 4) {
+#pragma unroll
+      for (int c = 0; c < NT; c += 16) {
+        int v[16];
+        tmem_ld16(tmem + lanes + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part[(c + e) * BR + 32 * warp + lane] = v[e];
+      }
+    }
+    cluster_sync();
+    if (warp < 4) {
+      const unsigned mine = smem_u32(part + 32 * warp + lane);
+      unsigned from[MAX_SPLIT];
+#pragma unroll
+      for (int s = 0; s < MAX_SPLIT; ++s) from[s] = s < split ? map_to_rank(mine, s) : 0u;
+      // NT / split columns a CTA (NT >= 16, split a power of two up to 8)
+      const int nc = NT / split;
+      for (int c = rank * nc; c < (rank + 1) * nc; c += 2) {
+        int v[2] = {0, 0}, got[2][MAX_SPLIT];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int s = 0; s < MAX_SPLIT; ++s) {
+            got[j][s] = 0;
+            if (s < split)
+              asm volatile("ld.shared::cluster.s32 %0, [%1];\n"
+                           : "=r"(got[j][s])
+                           : "r"(from[s] + (unsigned)((c + j) * BR * 4))
+                           : "memory");
+          }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int s = 0; s < MAX_SPLIT; ++s) v[j] += got[j][s];
+        if (!ctl.abort)
+          store_columns<T, 2>(p, v, row0 + 32 * warp, lane, col0 + c, rscale, rbias);
+      }
+    }
+    cluster_sync();  // every peer has read this CTA's sums
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+  __syncthreads();
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(TMEM)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ launching
+
+bool tma_rows(const int8_t *p, int64_t stride, int rows, int K) {
+  return aligned_to(p, 16) && (rows == 1 || (stride % 16 == 0 && stride >= K));
+}
+
+// [rows, K] bytes, box 128 bytes x box_rows, 128-byte swizzle; bytes past K
+// and rows past the last read as zero.
+bv_status encode_rows(CUtensorMap *map, const int8_t *p, int64_t stride, int rows, int K,
+                      int box_rows) {
+  if (!encode_fn()) return fail(BV_ERR_UNSUPPORTED, "bv_int8_matmul: no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(rows == 1 ? (K + 15) / 16 * 16 : stride)};
+  const cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(p), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(BV_ERR_CUDA, "bv_int8_matmul: tensor map (%d)", (int)r);
+  return BV_OK;
+}
+
+template <typename T, int NT, bool TMA>
+bv_status run_tile(const Mm &p, cudaStream_t st) {
+  const int64_t tiles_r = ((int64_t)p.rows + BR - 1) / BR, tiles_c = ((int64_t)p.cols + NT - 1) / NT;
+  const int64_t tiles = tiles_r * tiles_c;
+  const int chunks = (p.K + BK - 1) / BK;
+  int split = 1;
+  while (split < MAX_SPLIT && tiles * split * 2 <= 296 && chunks >= 4 * split) split *= 2;
+  if (tiles * split > 0x7fffffff) return fail(BV_ERR_SHAPE, "bv_int8_matmul: grid");
+  constexpr int STAGE = tile_stage_bytes<NT>();
+  const int per = (chunks + split - 1) / split;
+  // two CTAs an SM; room for the partial sums of a split tile
+  int stages = std::min(std::min(per, TILE_MAX_STAGES), (112 * 1024 - 1024) / STAGE);
+  const int least = split > 1 ? (NT * BR * 4 + STAGE - 1) / STAGE : 1;
+  stages = std::max(stages, least);
+  const size_t smem = (size_t)stages * STAGE + 1024;
+  auto kernel = int8_tile_kernel<T, NT, TMA>;
+  BV_TRY(ensure_dynamic_smem((const void *)kernel, smem, "bv_int8_matmul smem"));
+  CUtensorMap mr{}, mc{};
+  if (TMA) {
+    BV_TRY(encode_rows(&mr, p.r, p.rstride, p.rows, p.K, BR));
+    BV_TRY(encode_rows(&mc, p.c, p.cstride, p.cols, p.K, NT));
+  }
+  int *status = device_status_ptr();
+  if (!status) return fail(BV_ERR_CUDA, "bv_int8_matmul: status word");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(TMA ? 128 : 256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)split, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, mr, mc, p, (int)tiles_r, split, stages, status,
+                              wait_limit()));
+  return BV_OK;
+}
+
+template <typename T, bool TMA>
+bv_status run_typed(const Mm &p, cudaStream_t st) {
+  if (p.cols <= 16) return run_tile<T, 16, TMA>(p, st);
+  if (p.cols <= 32) return run_tile<T, 32, TMA>(p, st);
+  if (p.cols <= 64) return run_tile<T, 64, TMA>(p, st);
+  return run_tile<T, 128, TMA>(p, st);
 }
 
 }  // namespace
 
-bv_status launch_int8_matmul(const Int8Args &p, int dtype, cudaStream_t st) {
-  if (p.M == 0 || p.N == 0) return BV_OK;
-  const int64_t tm = (p.M + TILE - 1) / TILE, tn = (p.N + TILE - 1) / TILE;
-  if (tm * tn > 0x7fffffff) return fail(BV_ERR_SHAPE, "bv_int8_matmul: grid");
-  const double out = (double)p.M * p.N;
+bv_status launch_int8_matmul(const Int8Args &a, int dtype, cudaStream_t st) {
+  if (a.M == 0 || a.N == 0) return BV_OK;
+  Mm p{};
+  const bool cf = a.channels_first != 0;
+  p.r = cf ? a.a : a.w;
+  p.c = cf ? a.w : a.a;
+  p.rstride = cf ? a.as : a.ws;
+  p.cstride = cf ? a.ws : a.as;
+  p.rows = cf ? a.M : a.N;
+  p.cols = cf ? a.N : a.M;
+  p.K = a.K;
+  p.r_scale = cf ? a.a_scale : a.w_scale;
+  p.c_scale = cf ? a.w_scale : a.a_scale;
+  p.r_bias = cf ? nullptr : a.bias;
+  p.c_bias = cf ? a.bias : nullptr;
+  p.residual = a.residual;
+  p.y = a.y;
+  p.rs = a.rs;
+  p.ys = a.ys;
+  p.pairs = aligned_to(a.y, 4) && (a.ys % 2 == 0 || p.cols == 1);
+  const bool tma = tma_rows(p.r, p.rstride, p.rows, p.K) && tma_rows(p.c, p.cstride, p.cols, p.K);
+  const double out = (double)a.M * a.N;
   {
-    LaunchTimer t(st, "int8_matmul", 2.0 * out * p.K,
-                  ((double)p.M + p.N) * p.K + out * dtype_size(dtype) * (p.residual ? 2 : 1));
-    const unsigned grid = (unsigned)(tm * tn);
-    if (dtype == BV_F32) int8_tile_kernel<float><<<grid, 256, 0, st>>>(p, (int)tm);
-    else if (dtype == BV_BF16) int8_tile_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, (int)tm);
-    else int8_tile_kernel<__half><<<grid, 256, 0, st>>>(p, (int)tm);
+    LaunchTimer t(st, "int8_matmul", 2.0 * out * a.K,
+                  ((double)a.M + a.N) * a.K + out * dtype_size(dtype) * (a.residual ? 2 : 1));
+    if (dtype == BV_F32)
+      BV_TRY((tma ? run_typed<float, true>(p, st) : run_typed<float, false>(p, st)));
+    else if (dtype == BV_BF16)
+      BV_TRY((tma ? run_typed<__nv_bfloat16, true>(p, st)
+                  : run_typed<__nv_bfloat16, false>(p, st)));
+    else
+      BV_TRY((tma ? run_typed<__half, true>(p, st) : run_typed<__half, false>(p, st)));
   }
   count_launch();
   return check_launch("int8_matmul");
@@ -89,7 +491,8 @@ bv_status bv_int8_matmul(const int8_t *a, int64_t a_stride, const float *a_scale
   const char *what = "bv_int8_matmul";
   clear_error();
   if (!dtype_ok(dtype)) return fail(BV_ERR_ARG, "%s: dtype %d", what, dtype);
-  if (M < 0 || N < 1 || K < 1 || K > BV_INT8_MAX_DEPTH)
+  constexpr int kMaxRows = 0x7fffff00;  // tile indexes stay inside 32 bits
+  if (M < 0 || M > kMaxRows || N < 1 || N > kMaxRows || K < 1 || K > BV_INT8_MAX_DEPTH)
     return fail(BV_ERR_SHAPE, "%s: M=%d N=%d K=%d", what, M, N, K);
   const int64_t max_stride = (int64_t)1 << 28;  // rows (below 2^31) x stride x 4 bytes < 2^62
   if (a_stride < 0 || a_stride > max_stride || w_stride < 0 || w_stride > max_stride ||
