@@ -82,52 +82,56 @@ __device__ __forceinline__ unsigned bits16(__nv_bfloat16 v) { return __bfloat16_
 __device__ __forceinline__ unsigned bits16(__half v) { return __half_as_ushort(v); }
 __device__ __forceinline__ unsigned bits16(float) { return 0; }
 
-// A warp's 32 rows (row0 + lane) x N columns from col0 of the accumulator go
-// out: `rscale`, `rbias` are this lane's row's.  The residual's loads are
-// issued before the first store (it may be y: each element is read by the
-// thread that writes it, in this call).  A 16-bit column is half a word a
-// lane, so lanes swap halves in pairs: the even one writes two rows of the
-// even column, the odd one two rows of the odd column.
+// The residual of a warp's 32 rows (row0 + lane) x N columns from col0 on.
+template <typename T, int N>
+__device__ __forceinline__ void load_residual(const Mm &p, int row0, int lane, int col0, T (&r)[N]) {
+  if (!p.residual || row0 + lane >= p.rows) return;
+  const T *res = static_cast<const T *>(p.residual) + (int64_t)col0 * p.rs + row0 + lane;
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (col0 + e < p.cols) r[e] = res[e * p.rs];
+}
+
+// Those columns of the accumulator go out: `rscale`, `rbias` are this lane's
+// row's, cs and cb (shared memory, 8-byte aligned) the columns' scales and biases,
+// cb zeros where the bias belongs to the rows.  The residual (`r`) was loaded
+// before; it may be y, as each element is read by the thread that writes it.
+// A 16-bit column is half a word a lane, so lanes swap halves in pairs: the
+// even one writes two rows of the even column, the odd one two rows of the odd
+// column.
 template <typename T, int N>
 __device__ __forceinline__ void store_columns(const Mm &p, const int (&acc)[N], int row0, int lane,
-                                              int col0, float rscale, float rbias) {
-  static_assert(N <= 32 && N % 2 == 0, "one column's scale a lane");
-  const int row = row0 + lane;
+                                              int col0, float rscale, float rbias, const float *cs,
+                                              const float *cb, const T (&r)[N]) {
+  static_assert(N % 2 == 0, "columns go out in pairs");
   const int nc = min(N, p.cols - col0);  // warp-uniform
   if (row0 >= p.rows || nc <= 0) return;
+  const int row = row0 + lane;
   const bool in = row < p.rows;
-  const bool mine = lane < nc;
-  const float cs = mine ? __ldg(p.c_scale + col0 + lane) : 0.0f;
-  const float cb = mine && p.c_bias ? __ldg(p.c_bias + col0 + lane) : 0.0f;
-  T *y = static_cast<T *>(p.y) + (int64_t)col0 * p.ys + row;
-  const T *res = static_cast<const T *>(p.residual) + (int64_t)col0 * p.rs + row;
-  T r[N];
-  if (p.residual) {
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (in && e < nc) r[e] = res[e * p.rs];
-  }
   const bool pairs = sizeof(T) == 2 && p.pairs && row0 + 32 <= p.rows;
+  const int odd = pairs ? lane & 1 : 0;
+  T *y = static_cast<T *>(p.y) + (int64_t)(col0 + odd) * p.ys + (row - odd);
 #pragma unroll
-  for (int e = 0; e < N; e += 2) {
-    T v[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float s = rscale * __shfl_sync(0xffffffffu, cs, e + j);
-      float f = fmaf((float)acc[e + j], s, rbias + __shfl_sync(0xffffffffu, cb, e + j));
-      if (p.residual && in && e + j < nc) f += to_f32(r[e + j]);
-      v[j] = from_f32<T>(f);
-    }
+  for (int e = 0; e < N; e += 2, y += 2 * p.ys) {
+    const float2 s = mul2(*reinterpret_cast<const float2 *>(cs + e), both(rscale));
+    const float2 b = add2(*reinterpret_cast<const float2 *>(cb + e), both(rbias));
+    float2 f = fma2(make_float2((float)acc[e], (float)acc[e + 1]), s, b);
+    if (p.residual) f = add2(f, make_float2(to_f32(r[e]), to_f32(r[e + 1])));
     if (pairs) {
-      const int odd = lane & 1;
-      const unsigned got = __shfl_xor_sync(0xffffffffu, odd ? bits16(v[0]) : bits16(v[1]), 1);
+      T v[2] = {from_f32<T>(f.x), from_f32<T>(f.y)};
+      const unsigned give = odd ? bits16(v[0]) : bits16(v[1]);
+      const unsigned got = __shfl_xor_sync(0xffffffffu, give, 1);
       const unsigned word = odd ? (got | (bits16(v[1]) << 16)) : (bits16(v[0]) | (got << 16));
-      if (e + odd < nc) *reinterpret_cast<unsigned *>(y + (e + odd) * p.ys - odd) = word;
+      if (e + odd < nc) *reinterpret_cast<unsigned *>(y) = word;
     } else if (in) {
-      if (e < nc) y[e * p.ys] = v[0];
-      if (e + 1 < nc) y[(e + 1) * p.ys] = v[1];
+      if (e < nc) y[0] = from_f32<T>(f.x);
+      if (e + 1 < nc) y[p.ys] = from_f32<T>(f.y);
     }
   }
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 __host__ __device__ constexpr int tmem_cols(int n) {
@@ -199,6 +203,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t bars[2 * TILE_MAX_STAGES + 1];
   __shared__ Ctl ctl;
+  __shared__ __align__(16) float cs[NT], cb[NT];  // the tile's columns' scales and biases
   const unsigned bar_full = smem_u32(&bars[0]);
   const unsigned bar_empty = smem_u32(&bars[TILE_MAX_STAGES]);
   const unsigned bar_done = smem_u32(&bars[2 * TILE_MAX_STAGES]);
@@ -211,6 +216,10 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   const WaitCtx wc{&ctl, 0u, status, wait_limit};
 
   if (threadIdx.x == 0) {
+    if (TMA) {
+      prefetch_map(&map_r);
+      prefetch_map(&map_c);
+    }
     ctl.abort = 0;
     for (int s = 0; s < stages; ++s) {
       mbar_init(bar_full + 8 * s, TMA ? 1 : 4);
@@ -230,6 +239,17 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
   const unsigned tmem = ctl.tmem;
+  // what the epilogue needs of the scales, on its way during the products
+  const int row = row0 + 32 * warp + lane;  // of warps 0..3
+  const bool in = warp < 4 && row < p.rows;
+  const float rscale = in ? __ldg(p.r_scale + row) : 0.0f;
+  const float rbias = in && p.r_bias ? __ldg(p.r_bias + row) : 0.0f;
+  if (warp == 2 || warp == 3)
+    for (int c = threadIdx.x - 64; c < NT; c += 64) {
+      const bool have = col0 + c < p.cols;
+      cs[c] = have ? __ldg(p.c_scale + col0 + c) : 0.0f;
+      cb[c] = have && p.c_bias ? __ldg(p.c_bias + col0 + c) : 0.0f;
+    }
 
   if (TMA && warp == 0 && lane == 0) {
     int c = 0;
@@ -297,23 +317,22 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   __syncwarp();
 
   if (warp < 4) {
+    asm volatile("bar.sync 1, 128;\n" ::: "memory");  // cs, cb
     warp_wait(bar_done, 0, wc, 304);
     asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
   }
   const unsigned lanes = (unsigned)(32 * warp) << 16;  // of warps 0..3
-  const int row = row0 + 32 * warp + lane;
-  const bool in = warp < 4 && row < p.rows;
-  const float rscale = in ? __ldg(p.r_scale + row) : 0.0f;
-  const float rbias = in && p.r_bias ? __ldg(p.r_bias + row) : 0.0f;
   if (split == 1) {
     if (warp < 4) {
 #pragma unroll
       for (int c = 0; c < NT; c += 16) {
         int v[16];
+        T r[16];
         tmem_ld16(tmem + lanes + c, v);
+        load_residual(p, row0 + 32 * warp, lane, col0 + c, r);
         tmem_wait_ld();
         if (!ctl.abort)
-          store_columns<T, 16>(p, v, row0 + 32 * warp, lane, col0 + c, rscale, rbias);
+          store_columns(p, v, row0 + 32 * warp, lane, col0 + c, rscale, rbias, cs + c, cb + c, r);
       }
     }
   } else {
@@ -339,6 +358,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
       const int nc = NT / split;
       for (int c = rank * nc; c < (rank + 1) * nc; c += 2) {
         int v[2] = {0, 0}, got[2][MAX_SPLIT];
+        T r[2];
+        load_residual(p, row0 + 32 * warp, lane, col0 + c, r);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -355,7 +376,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
 #pragma unroll
           for (int s = 0; s < MAX_SPLIT; ++s) v[j] += got[j][s];
         if (!ctl.abort)
-          store_columns<T, 2>(p, v, row0 + 32 * warp, lane, col0 + c, rscale, rbias);
+          store_columns(p, v, row0 + 32 * warp, lane, col0 + c, rscale, rbias, cs + c, cb + c, r);
       }
     }
     cluster_sync();  // every peer has read this CTA's sums
@@ -365,6 +386,229 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(TMEM)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------- many tiles
+//
+// Persistent CTA pairs: a pair's tile is 256 rows x NT columns (cta_group::2:
+// each CTA holds half of the rows and loads half of the columns), TMA fills a
+// ring of stages, and two accumulators of NT columns in TMEM let eight warps a
+// CTA write one tile out while the tensor cores work on the next.  Tiles are
+// walked in bands of BAND row tiles, so that the pairs at work at one time share
+// operand tiles in L2.
+
+constexpr int PAIR_THREADS = 384;
+constexpr int PAIR_EPI_WARPS = 8;
+constexpr int BAND = 8;
+
+template <int NT>
+constexpr int pair_stage_bytes() {
+  return (BR + NT / 2) * BK;
+}
+template <int NT>
+constexpr int pair_stages() {
+  return 200 * 1024 / pair_stage_bytes<NT>();
+}
+// Arrive at the even CTA's barrier: this warp's TMEM reads are complete.
+__device__ __forceinline__ void arrive_remote(unsigned cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr)
+               : "memory");
+}
+
+template <typename T, int NT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
+int8_pair_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_c,
+                 const Mm p, int tiles_r, int tiles_c, int *status, long long wait_limit) {
+  constexpr int STAGE = pair_stage_bytes<NT>(), STAGES = pair_stages<NT>();
+  constexpr unsigned TMEM = tmem_cols(2 * NT);
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t bars[2 * STAGES + 5];
+  __shared__ Ctl ctl;
+  __shared__ __align__(16) float cs[2][NT], cb[2][NT];  // columns' scales and biases, two tiles
+  // the even CTA's full and free barriers serve the pair
+  const unsigned bar_full = smem_u32(&bars[0]), bar_empty = smem_u32(&bars[STAGES]);
+  const unsigned bar_acc = smem_u32(&bars[2 * STAGES]), bar_free = smem_u32(&bars[2 * STAGES + 2]);
+  const unsigned bar_done = smem_u32(&bars[2 * STAGES + 4]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pairs = (int)(gridDim.x >> 1), pid = (int)(blockIdx.x >> 1);
+  const int n_tiles = tiles_r * tiles_c;
+  const int chunks = (p.K + BK - 1) / BK;
+  const WaitCtx wc{&ctl, map_to_rank(smem_u32(&ctl.abort), rank ^ 1u), status, wait_limit};
+  auto tile_at = [&](int tau, int &row0, int &col0) {
+    const int band = tau / (BAND * tiles_c), in = tau - band * BAND * tiles_c;
+    const int high = min(BAND, tiles_r - band * BAND);
+    row0 = (band * BAND + in % high) * 2 * BR + (int)rank * BR;  // this CTA's rows
+    col0 = in / high * NT;
+  };
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_r);
+    prefetch_map(&map_c);
+    ctl.abort = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_acc + 8 * s, 1);
+      mbar_init(bar_free + 8 * s, 2 * PAIR_EPI_WARPS);
+    }
+    mbar_init(bar_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+                     smem_u32(&ctl.tmem)),
+                 "n"(TMEM)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+  cluster_sync();  // both CTAs' barriers exist before anyone signals them
+  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+  const unsigned tmem = ctl.tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      unsigned pass = 0;  // over the ring
+      bool ok = true;
+      for (int tau = pid; tau < n_tiles && ok; tau += pairs) {
+        int row0, col0;
+        tile_at(tau, row0, col0);
+        for (int c = 0; c < chunks; ++c) {
+          if (pass > 0 && !mbar_wait(bar_empty + 8 * s, (pass - 1) & 1, wc, 311)) {
+            ok = false;
+            break;
+          }
+          const unsigned dst = smem_u32(smem + s * STAGE), fb = bar_full + 8 * s;
+          if (leader) mbar_arrive_tx(fb, 2 * STAGE);
+          tma_load_2d_pair(dst, &map_r, c * BK, row0, fb);
+          tma_load_2d_pair(dst + BR * BK, &map_c, c * BK, col0 + (int)rank * (NT / 2), fb);
+          ++issued;
+          if (++s == STAGES) {
+            s = 0;
+            ++pass;
+          }
+        }
+      }
+      // the pair's last load into each slot has landed before the CTA can
+      // exit (the even CTA's barriers count both CTAs' bytes, and the final
+      // cluster barrier holds the odd CTA until then)
+      if (leader)
+        for (int d = issued - STAGES; d < issued; ++d)
+          if (d >= 0) mbar_drain(bar_full + 8 * (d % STAGES), (d / STAGES) & 1);
+    }
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      int s = 0, it = 0;  // ring slot, tiles begun
+      unsigned phase = 0;
+      bool ok = true;
+      for (int tau = pid; tau < n_tiles && ok; tau += pairs, ++it) {
+        const int buf = it & 1;
+        if (it >= 2 && !mbar_wait(bar_free + 8 * buf, (it / 2 - 1) & 1, wc, 312)) break;
+        asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+        const unsigned acc = tmem + (unsigned)(buf * NT);
+        for (int c = 0; c < chunks; ++c) {
+          if (!mbar_wait(bar_full + 8 * s, phase, wc, 313)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+          const unsigned at = smem_u32(smem + s * STAGE);
+          const uint64_t da = sw128_desc(at), db = sw128_desc(at + BR * BK);
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            mma_i8<2>(acc, da + 2 * k, db + 2 * k, i8_idesc(2 * BR, NT), c > 0 || k > 0 ? 1u : 0u);
+          mma_commit_pair(bar_empty + 8 * s);
+          if (++s == STAGES) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) mma_commit_pair(bar_acc + 8 * buf);
+      }
+      // every MMA issued above has completed before TMEM can be freed
+      mma_commit_pair(bar_done);
+      mbar_drain(bar_done, 0);
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., half of the columns
+    const int ct = threadIdx.x - 128;                // column whose scale this thread fetches
+    const unsigned free_leader = map_to_rank(bar_free, 0);
+    // a tile's scales and biases are fetched while the tile before it goes out
+    float n_cs = 0.0f, n_cb = 0.0f, n_rs = 0.0f, n_rb = 0.0f;
+    auto fetch = [&](int tau) {
+      if (tau >= n_tiles) return;
+      int row0, col0;
+      tile_at(tau, row0, col0);
+      const int row = row0 + 32 * q + lane, col = col0 + ct;
+      n_rs = row < p.rows ? __ldg(p.r_scale + row) : 0.0f;
+      n_rb = row < p.rows && p.r_bias ? __ldg(p.r_bias + row) : 0.0f;
+      const bool have = ct < NT && col < p.cols;
+      n_cs = have ? __ldg(p.c_scale + col) : 0.0f;
+      n_cb = have && p.c_bias ? __ldg(p.c_bias + col) : 0.0f;
+    };
+    fetch(pid);
+    int it = 0;
+    // after a wait that gave up the warp still takes every barrier, and writes
+    // nothing
+    bool alive = true;
+    for (int tau = pid; tau < n_tiles; tau += pairs, ++it) {
+      int row0, col0;
+      tile_at(tau, row0, col0);
+      row0 += 32 * q;
+      const int buf = it & 1;
+      const float rscale = n_rs, rbias = n_rb;
+      if (ct < NT) {
+        cs[buf][ct] = n_cs;
+        cb[buf][ct] = n_cb;
+      }
+      fetch(tau + pairs);
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");  // cs, cb of this tile
+      const int c0 = half * (NT / 2);
+      T r[2][16];
+      load_residual(p, row0, lane, col0 + c0, r[0]);
+      if (!warp_wait(bar_acc + 8 * buf, (it >> 1) & 1, wc, 314)) alive = false;
+      asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+      const unsigned acc = tmem + ((unsigned)(32 * q) << 16) + (unsigned)(buf * NT + c0);
+      int v[2][16];
+      tmem_ld16(acc, v[0]);
+#pragma unroll
+      for (int c = 0; c < NT / 2; c += 16) {
+        const int now = (c >> 4) & 1, next = now ^ 1;
+        tmem_wait_ld();
+        if (c + 16 < NT / 2) {
+          tmem_ld16(acc + c + 16, v[next]);
+          load_residual(p, row0, lane, col0 + c0 + c + 16, r[next]);
+        } else {
+          asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+          __syncwarp();
+          if (lane == 0) arrive_remote(free_leader + 8 * buf);
+        }
+        if (alive)
+          store_columns(p, v[now], row0, lane, col0 + c0 + c, rscale, rbias, cs[buf] + c0 + c,
+                        cb[buf] + c0 + c, r[now]);
+      }
+    }
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+  __syncthreads();
+  // after an abort the odd CTA may have loads in flight that the even CTA's
+  // barriers did not count; they land in a few microseconds
+  if (!leader && threadIdx.x == 0 && ctl.abort)
+    for (int i = 0; i < 64; ++i) __nanosleep(1000);
+  cluster_sync();  // no MMA, remote arrive or copy of the pair is in flight
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(TMEM)
                  : "memory");
   }
 }
@@ -398,12 +642,20 @@ bv_status run_tile(const Mm &p, cudaStream_t st) {
   const int64_t tiles = tiles_r * tiles_c;
   const int chunks = (p.K + BK - 1) / BK;
   int split = 1;
+#ifdef BV_INT8_SWEEP
+  split = sweep_split;
+  while (split > 1 && chunks < 2 * split) split /= 2;
+#else
   while (split < MAX_SPLIT && tiles * split * 2 <= 296 && chunks >= 4 * split) split *= 2;
+#endif
   if (tiles * split > 0x7fffffff) return fail(BV_ERR_SHAPE, "bv_int8_matmul: grid");
   constexpr int STAGE = tile_stage_bytes<NT>();
   const int per = (chunks + split - 1) / split;
   // two CTAs an SM; room for the partial sums of a split tile
   int stages = std::min(std::min(per, TILE_MAX_STAGES), (112 * 1024 - 1024) / STAGE);
+#ifdef BV_INT8_SWEEP
+  stages = std::min(std::min(per, TILE_MAX_STAGES), (sweep_kb * 1024 - 1024) / STAGE);
+#endif
   const int least = split > 1 ? (NT * BR * 4 + STAGE - 1) / STAGE : 1;
   stages = std::max(stages, least);
   const size_t smem = (size_t)stages * STAGE + 1024;
@@ -431,8 +683,42 @@ bv_status run_tile(const Mm &p, cudaStream_t st) {
   return BV_OK;
 }
 
+template <typename T, int NT>
+bv_status run_pair(const Mm &p, cudaStream_t st) {
+  const int64_t tiles_r = ((int64_t)p.rows + 2 * BR - 1) / (2 * BR);
+  const int64_t tiles_c = ((int64_t)p.cols + NT - 1) / NT;
+  // (tile indexes run past the last by at most a grid)
+  if (tiles_r * tiles_c > 0x7fff0000 || tiles_c > 0x7fff0000 / BAND)
+    return fail(BV_ERR_SHAPE, "bv_int8_matmul: grid");
+  constexpr size_t smem = (size_t)pair_stages<NT>() * pair_stage_bytes<NT>() + 1024;
+  auto kernel = int8_pair_kernel<T, NT>;
+  BV_TRY(ensure_dynamic_smem((const void *)kernel, smem, "bv_int8_matmul smem"));
+  CUtensorMap mr, mc;
+  BV_TRY(encode_rows(&mr, p.r, p.rstride, p.rows, p.K, BR));
+  BV_TRY(encode_rows(&mc, p.c, p.cstride, p.cols, p.K, NT / 2));
+  int *status = device_status_ptr();
+  if (!status) return fail(BV_ERR_CUDA, "bv_int8_matmul: status word");
+  const int grid = 2 * (int)std::min<int64_t>(tiles_r * tiles_c, 74);
+  kernel<<<grid, PAIR_THREADS, smem, st>>>(mr, mc, p, (int)tiles_r, (int)tiles_c, status,
+                                           wait_limit());
+  return BV_OK;
+}
+
 template <typename T, bool TMA>
 bv_status run_typed(const Mm &p, cudaStream_t st) {
+#ifdef BV_INT8_SWEEP
+  if constexpr (TMA) {
+    if (sweep_nt == 256 && sweep_pair) return run_pair<T, 256>(p, st);
+    if (sweep_nt == 128 && sweep_pair) return run_pair<T, 128>(p, st);
+  }
+  if (sweep_nt == 16) return run_tile<T, 16, TMA>(p, st);
+  if (sweep_nt == 32) return run_tile<T, 32, TMA>(p, st);
+  if (sweep_nt == 64) return run_tile<T, 64, TMA>(p, st);
+  return run_tile<T, 128, TMA>(p, st);
+#endif
+  if constexpr (TMA) {
+    if (p.cols > 128 && (int64_t)p.rows * p.cols > (int64_t)1 << 21) return run_pair<T, 256>(p, st);
+  }
   if (p.cols <= 16) return run_tile<T, 16, TMA>(p, st);
   if (p.cols <= 32) return run_tile<T, 32, TMA>(p, st);
   if (p.cols <= 64) return run_tile<T, 64, TMA>(p, st);

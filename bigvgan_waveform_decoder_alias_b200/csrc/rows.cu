@@ -13,6 +13,9 @@
 // the registers of one warp or one block between its only read and its write;
 // the sum of squares and the maximum go through one reduction together.  Rows
 // past the registers of a block are read twice.
+#include <algorithm>
+
+#include "tc_ptx.cuh"
 #include "token_types.cuh"
 
 namespace bv {
@@ -20,60 +23,84 @@ namespace {
 
 constexpr unsigned kInfBits = 0x7f800000u;
 
+// What a kernel writes: the norm in the rows' type, the norm in 8 bits, or the
+// rows themselves in 8 bits.
+enum Mode { kNorm, kNorm8, kQuant };
+
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Pack {
   T v[N];
 };
 
-// N values at p, `valid` of them in range (the others 0).  Plain loads: the
-// rows may be overwritten by this kernel (sum may be x or the residual).
-template <typename T, int N>
-__device__ __forceinline__ Pack<T, N> load_pack(const T *p, int valid) {
-  Pack<T, N> r;
-  if (valid >= N) {
-    r = *reinterpret_cast<const Pack<T, N> *>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) r.v[i] = i < valid ? p[i] : from_f32<T>(0.0f);
-  }
+// The larger of m, |a| and |b|; NaN if one is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
   return r;
 }
-template <typename T, int N>
-__device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &r, int valid) {
-  if (valid >= N) {
-    *reinterpret_cast<Pack<T, N> *>(p) = r;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < valid) p[i] = r.v[i];
-  }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-__device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Elements 2 p and 2 p + 1 of a pack, and back (rounded).
+template <int N>
+__device__ __forceinline__ float2 get2(const Pack<float, N> &v, int p) {
+  return make_float2(v.v[2 * p], v.v[2 * p + 1]);
+}
+template <int N>
+__device__ __forceinline__ float2 get2(const Pack<__nv_bfloat16, N> &v, int p) {
+  const unsigned w = reinterpret_cast<const unsigned *>(&v)[p];
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <int N>
+__device__ __forceinline__ float2 get2(const Pack<__half, N> &v, int p) {
+  return __half22float2(reinterpret_cast<const __half2 *>(&v)[p]);
+}
+template <int N>
+__device__ __forceinline__ void set2(Pack<float, N> &v, int p, float2 f) {
+  v.v[2 * p] = f.x;
+  v.v[2 * p + 1] = f.y;
+}
+template <int N>
+__device__ __forceinline__ void set2(Pack<__nv_bfloat16, N> &v, int p, float2 f) {
+  reinterpret_cast<__nv_bfloat162 *>(&v)[p] = __floats2bfloat162_rn(f.x, f.y);
+}
+template <int N>
+__device__ __forceinline__ void set2(Pack<__half, N> &v, int p, float2 f) {
+  reinterpret_cast<__half2 *>(&v)[p] = __floats2half2_rn(f.x, f.y);
+}
 
-// Sum of `s` and maximum of `m` over the row's threads (a warp, or the block),
-// in every thread.  `buf` alternates between calls, so one barrier is enough.
+// Sum of `s` and maximum of `m` (not negative, or NaN) over the row's threads,
+// in every thread: the block, or `tpr` lanes of a warp.  `buf` alternates
+// between calls, so one barrier is enough.
 struct Red {
-  float s[2][32];
-  unsigned m[2][32];
+  float s[2][32], m[2][32];
 };
 template <bool BLOCK>
-__device__ __forceinline__ void reduce_row(float &s, unsigned &m, Red &red, int &buf) {
+__device__ __forceinline__ void reduce_row(float &s, float &m, Red &red, int &buf, int tpr) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  m = __reduce_max_sync(0xffffffffu, m);
+  for (int o = 16; o > 0; o >>= 1)
+    if (BLOCK || o < tpr) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
   if constexpr (BLOCK) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (nw == 1) return;
     if (lane == 0) {
       red.s[buf][warp] = s;
       red.m[buf][warp] = m;
     }
     __syncthreads();
     s = lane < nw ? red.s[buf][lane] : 0.0f;
-    m = lane < nw ? red.m[buf][lane] : 0u;
+    m = lane < nw ? red.m[buf][lane] : 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    m = __reduce_max_sync(0xffffffffu, m);
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
     buf ^= 1;
   }
 }
@@ -87,12 +114,11 @@ __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) <
 struct Quant {
   float pre, inv, scale;
 };
-__device__ __forceinline__ Quant make_quant(unsigned abits, float rstd) {
+__device__ __forceinline__ Quant make_quant(float a, float rstd) {
   Quant r{1.0f, 0.0f, 0.0f};
-  if (abits >= kInfBits) {
+  if (!(a < __uint_as_float(kInfBits))) {
     r.scale = __int_as_float(0x7fc00000);
-  } else if (abits != 0) {
-    float a = __uint_as_float(abits);
+  } else if (a != 0.0f) {
     float back = 1.0f;
     if (a < pow2(-100)) {
       r.pre = pow2(64);
@@ -104,10 +130,32 @@ __device__ __forceinline__ Quant make_quant(unsigned abits, float rstd) {
   }
   return r;
 }
-__device__ __forceinline__ int8_t quantise(float t, const Quant &z) {
-  // rint(t inv) is within [-127, 127]: |t| <= a, and a (127 / a) is off by at
-  // most two roundings.  inv = 0 marks a row of zeros or of no finite scale.
-  return z.inv == 0.0f ? (int8_t)0 : (int8_t)__float2int_rn(__fmul_rn(t * z.pre, z.inv));
+
+// rint(v) in the lowest byte, for |v| <= 128: adding 1.5 2^23 rounds to the
+// nearest whole number, ties to even, and leaves it in the sum's low bits.
+// (t inv is within [-127, 127] but for two roundings.)
+constexpr float kRound = 12582912.0f;
+// N values as bytes; none where the row has no scale (inv = 0).
+template <int P>
+__device__ __forceinline__ uint64_t quantise(const float2 (&t)[P], const Quant &z) {
+  if (z.inv == 0.0f) return 0;
+  unsigned w[2] = {0, 0};
+#pragma unroll
+  for (int p = 0; p < P; p += 2) {
+    float2 a = t[p], b = t[p + 1];
+    if (z.pre != 1.0f) {
+      a = mul2(a, both(z.pre));
+      b = mul2(b, both(z.pre));
+    }
+    // (the packed product and sum would become one fma, with one rounding)
+    a = mul2(a, both(z.inv));
+    b = mul2(b, both(z.inv));
+    auto bits_of = [](float v) { return __float_as_uint(__fadd_rn(v, kRound)); };
+    const unsigned lo = __byte_perm(bits_of(a.x), bits_of(a.y), 0x0040);
+    const unsigned hi = __byte_perm(bits_of(b.x), bits_of(b.y), 0x0040);
+    w[p / 2] = __byte_perm(lo, hi, 0x5410);
+  }
+  return (uint64_t)w[0] | ((uint64_t)w[1] << 32);
 }
 
 // 1 / sqrt(mean + eps) of a row whose sum of squares is `s`.
@@ -115,223 +163,500 @@ __device__ __forceinline__ float row_rstd(float s, int cols, float eps) {
   return __frsqrt_rn(__fadd_rn(__fdiv_rn(s, (float)cols), eps));
 }
 
-// A thread holds NV groups of VEC values, group i at VEC (tid + i threads).
-// BLOCK: a block a row; else a warp a row.
-template <typename T, typename G, int VEC, int NV, bool BLOCK, bool NORM>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 128) rows_kernel(NormArgs a) {
-  __shared__ Red red;
-  const int tpr = BLOCK ? blockDim.x : 32;
-  const int tid = BLOCK ? threadIdx.x : (threadIdx.x & 31);
-  const int64_t row0 =
-      BLOCK ? blockIdx.x : blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int64_t step = BLOCK ? gridDim.x : gridDim.x * (int64_t)(blockDim.x >> 5);
-  int buf = 0;
-  Pack<G, VEC> g[NV];
-  if (NORM && a.gain) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = VEC * (tid + i * tpr);
-      if (c < a.cols) g[i] = load_pack<G, VEC>(static_cast<const G *>(a.gain) + c, a.cols - c);
-    }
+// How a row lies on its `tpr` threads: NV groups of VEC values each, group i at
+// VEC (tid + i tpr) - m.  RAGGED: cols is no multiple of VEC, or the rows of x,
+// residual, sum and y start m values past a 16-byte boundary (the same m in
+// one row, another in the next); groups follow the boundaries, so that all but
+// a row's two ends move 16 bytes at a time.
+template <int VEC, bool RAGGED>
+struct Lay {
+  int tid, tpr, m, cols;
+  __device__ __forceinline__ int first(int i) const {
+    return VEC * (tid + i * tpr) - (RAGGED ? m : 0);
   }
-  for (int64_t row = row0; row < a.rows; row += step) {
-    float h[NV][VEC];
-    {
-      const T *x = static_cast<const T *>(a.x) + row * a.xs;
-      const T *r = static_cast<const T *>(a.residual) + row * a.rs;
-      Pack<T, VEC> px[NV], pr[NV];
+  __device__ __forceinline__ bool some(int i) const { return first(i) < cols; }
+  __device__ __forceinline__ bool whole(int i) const {
+    return RAGGED ? first(i) + VEC <= cols && first(i) >= 0 : first(i) < cols;
+  }
+  __device__ __forceinline__ bool has(int i, int e) const {
+    return (!RAGGED || first(i) + e >= 0) && first(i) + e < cols;
+  }
+};
+
+// Group i of a row straight from memory (zero outside the row).  Plain loads:
+// the row may be overwritten by this kernel.
+template <typename T, int VEC, bool RAGGED>
+__device__ __forceinline__ Pack<T, VEC> load_group(const T *row, const Lay<VEC, RAGGED> &l, int i) {
+  Pack<T, VEC> p;
+  if (l.whole(i)) {
+    p = *reinterpret_cast<const Pack<T, VEC> *>(row + l.first(i));
+  } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = VEC * (tid + i * tpr);
-        if (c < a.cols) px[i] = load_pack<T, VEC>(x + c, a.cols - c);
-        if (NORM && a.residual && c < a.cols) pr[i] = load_pack<T, VEC>(r + c, a.cols - c);
-      }
+    for (int e = 0; e < VEC; ++e)
+      p.v[e] = RAGGED && l.has(i, e) ? row[l.first(i) + e] : from_f32<T>(0.0f);
+  }
+  return p;
+}
+template <typename T, int VEC, bool RAGGED>
+__device__ __forceinline__ void store_group(T *row, const Lay<VEC, RAGGED> &l, int i,
+                                            const Pack<T, VEC> &o) {
+  if (l.whole(i)) {
+    *reinterpret_cast<Pack<T, VEC> *>(row + l.first(i)) = o;
+  } else if (RAGGED) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool in = VEC * (tid + i * tpr) < a.cols;
+    for (int e = 0; e < VEC; ++e)
+      if (l.has(i, e)) row[l.first(i) + e] = o.v[e];
+  }
+}
+// Gain of group i.  Only its elements' alignment is known where RAGGED.
+template <typename G, int VEC, bool RAGGED>
+__device__ __forceinline__ Pack<G, VEC> load_gain(const G *gain, const Lay<VEC, RAGGED> &l, int i) {
+  Pack<G, VEC> g;
+  if constexpr (!RAGGED) {
+    if (l.whole(i)) g = *reinterpret_cast<const Pack<G, VEC> *>(gain + l.first(i));
+  } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          h[i][e] = in ? to_f32(px[i].v[e]) : 0.0f;
-          if (NORM && a.residual && in) h[i][e] += to_f32(pr[i].v[e]);
-        }
-      }
+    for (int e = 0; e < VEC; ++e)
+      g.v[e] = l.has(i, e) ? __ldg(gain + l.first(i) + e) : from_f32<G>(0.0f);
+  }
+  return g;
+}
+
+// Writes a group's VEC 8-bit values, the bytes of `word`.  q's rows start on
+// VEC bytes, so where RAGGED the group that q stores whole, [c0, c0 + VEC), is
+// the upper part of this thread's word and the lower part of the next one's;
+// where a warp or a row ends the parts go out by bytes.  Every lane of the warp
+// calls this.
+template <int VEC, bool RAGGED>
+__device__ __forceinline__ void store_q(int8_t *q, uint64_t word, const Lay<VEC, RAGGED> &l, int i) {
+  const int c0 = VEC * (l.tid + i * l.tpr);
+  auto whole_store = [&](uint64_t w) {
+    if constexpr (VEC == 8) *reinterpret_cast<uint64_t *>(q + c0) = w;
+    else *reinterpret_cast<unsigned *>(q + c0) = (unsigned)w;
+  };
+  if constexpr (!RAGGED) {
+    if (l.whole(i)) whole_store(word);
+  } else {
+    const int lane = threadIdx.x & 31, m = l.m;
+    const uint64_t next = __shfl_down_sync(0xffffffffu, word, 1);
+    const bool low = lane == 0 || l.tid == 0, high = lane == 31 || l.tid == l.tpr - 1;
+    if (low) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e < m && l.has(i, e)) q[c0 - m + e] = (int8_t)(word >> (8 * e));
     }
-    auto t_of = [&](int i, int e) {
-      return NORM && a.gain ? __fmul_rn(h[i][e], to_f32(g[i].v[e])) : h[i][e];
-    };
-    float s = 0.0f;
-    unsigned m = 0;
+    const uint64_t all =
+        m == 0 ? word : (word >> (8 * m)) | (high ? 0 : next << (8 * (VEC - m)));
+    const int n = min(l.cols - c0, high ? VEC - m : VEC);  // values of [c0, c0 + VEC) in hand
+    if (n >= VEC) {
+      whole_store(all);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = VEC * (tid + i * tpr);
-      if (c < a.cols) {
-        if (NORM && a.sum) {
-          Pack<T, VEC> o;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) o.v[e] = from_f32<T>(h[i][e]);
-          store_pack<T, VEC>(static_cast<T *>(a.sum) + row * a.ss + c, o, a.cols - c);
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (NORM) s = fmaf(h[i][e], h[i][e], s);
-          if (a.q && c + e < a.cols) m = max(m, abs_bits(t_of(i, e)));
-        }
-      }
+      for (int e = 0; e < VEC; ++e)
+        if (e < n) q[c0 + e] = (int8_t)(all >> (8 * e));
     }
-    reduce_row<BLOCK>(s, m, red, buf);
-    float rstd = 1.0f;
-    if (NORM) {
-      rstd = row_rstd(s, a.cols, a.eps);
-      if (!(s < __uint_as_float(kInfBits))) {
-        // The squares overflowed: if every h is finite, scale the row by a
-        // power of two and sum again (hm is past 2^48 then, so that down is
-        // a normal number).
-        float s2 = 0.0f;
-        unsigned hm = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) hm = max(hm, abs_bits(h[i][e]));
-        reduce_row<BLOCK>(s2, hm, red, buf);
-        if (hm < kInfBits) {
-          const float down = pow2(167 - (int)(hm >> 23));  // the maximum to 2^40 .. 2^41
-          s2 = 0.0f;
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s2 = fmaf(h[i][e] * down, h[i][e] * down, s2);
-          unsigned none = 0;
-          reduce_row<BLOCK>(s2, none, red, buf);
-          rstd = row_rstd(s2, a.cols, a.eps * down * down) * down;
-        }
-      }
-    }
-    const Quant z = a.q ? make_quant(m, rstd) : Quant{1.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = VEC * (tid + i * tpr);
-      if (c < a.cols) {
-        if (NORM && a.y) {
-          Pack<T, VEC> o;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            // (h rstd) gain: h rstd is at most sqrt(cols), so it cannot overflow
-            float v = h[i][e] * rstd;
-            if (a.gain) v *= to_f32(g[i].v[e]);
-            o.v[e] = from_f32<T>(v);
-          }
-          store_pack<T, VEC>(static_cast<T *>(a.y) + row * a.ys + c, o, a.cols - c);
-        }
-        if (a.q) {
-          Pack<int8_t, VEC> o;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) o.v[e] = quantise(t_of(i, e), z);
-          store_pack<int8_t, VEC>(a.q + row * a.qs + c, o, a.cols - c);
-        }
-      }
-    }
-    if (a.q && tid == 0) a.scale[row] = z.scale;
   }
 }
 
-// Rows longer than a block's registers: one block a row, read twice (the
-// second time mostly from L2).  The sum is written on the second read, by the
-// thread that read its operands, so it may be x or the residual.
-template <typename T, typename G, bool NORM>
+// The row once its values h and gains g are in registers: sum, norm, outputs.
+// `freed()` runs after the row's first reduction, when every thread of the row
+// holds its values.
+template <typename T, typename G, int NV, bool BLOCK, Mode MODE, bool RAGGED, typename F>
+__device__ __forceinline__ void finish_row(const NormArgs &a, int64_t row,
+                                           const Lay<16 / (int)sizeof(T), RAGGED> &l,
+                                           const float2 (&h)[NV][8 / sizeof(T)],
+                                           const Pack<G, 16 / sizeof(T)> (&g)[NV], Red &red,
+                                           int &buf, F freed) {
+  constexpr int VEC = 16 / (int)sizeof(T), P = VEC / 2;
+  const bool gained = MODE != kQuant && a.gain;
+  float2 s2 = both(0.0f);
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (!l.some(i)) continue;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (MODE != kQuant) s2 = fma2(h[i][p], h[i][p], s2);
+      if (MODE != kNorm) {
+        const float2 t = gained ? mul2(h[i][p], get2(g[i], p)) : h[i][p];
+        top = max_abs(top, t.x, t.y);
+      }
+    }
+    if (MODE != kQuant && a.sum) {
+      Pack<T, VEC> o;
+#pragma unroll
+      for (int p = 0; p < P; ++p) set2(o, p, h[i][p]);
+      store_group(static_cast<T *>(a.sum) + row * a.ss, l, i, o);
+    }
+  }
+  float s = s2.x + s2.y;
+  reduce_row<BLOCK>(s, top, red, buf, l.tpr);
+  freed();
+  float rstd = 1.0f;
+  if (MODE != kQuant) {
+    rstd = row_rstd(s, a.cols, a.eps);
+    const bool over = !(s < __uint_as_float(kInfBits));
+    // (a block takes the branch as one; of a warp with several rows, all lanes
+    // take part for any of them)
+    if (BLOCK ? over : __any_sync(0xffffffffu, over)) {
+      // The squares overflowed: if every h is finite, scale the row by a
+      // power of two and sum again (hm is past 2^48 then, so that down is
+      // a normal number).
+      float hm = 0.0f, none = 0.0f, zero = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) hm = max_abs(hm, h[i][p].x, h[i][p].y);
+      reduce_row<BLOCK>(zero, hm, red, buf, l.tpr);
+      const bool finite = hm < __uint_as_float(kInfBits);
+      const float down =
+          over && finite ? pow2(167 - (int)(__float_as_uint(hm) >> 23)) : 1.0f;  // to 2^40 .. 2^41
+      float2 d2 = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const float2 v = mul2(h[i][p], both(down));
+          d2 = fma2(v, v, d2);
+        }
+      float d = d2.x + d2.y;
+      reduce_row<BLOCK>(d, none, red, buf, l.tpr);
+      if (over && finite) rstd = row_rstd(d, a.cols, a.eps * down * down) * down;
+    }
+  }
+  if constexpr (MODE == kNorm) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!l.some(i)) continue;
+      Pack<T, VEC> o;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        // (h rstd) gain: h rstd is at most sqrt(cols), it cannot overflow
+        float2 v = mul2(h[i][p], both(rstd));
+        if (gained) v = mul2(v, get2(g[i], p));
+        set2(o, p, v);
+      }
+      store_group(static_cast<T *>(a.y) + row * a.ys, l, i, o);
+    }
+  } else {
+    const Quant z = make_quant(top, rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float2 t[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) t[p] = gained ? mul2(h[i][p], get2(g[i], p)) : h[i][p];
+      store_q(a.q + row * a.qs, quantise(t, z), l, i);
+    }
+    if (l.tid == 0 && l.cols > 0) a.scale[row] = z.scale;
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ int shift_of(const T *row) {
+  return (int)((reinterpret_cast<uintptr_t>(row) / sizeof(T)) & (uintptr_t)(VEC - 1));
+}
+
+// Few rows, or short ones: each goes from memory into the registers of a block
+// (BLOCK) or of `tpr` lanes.
+template <typename T, typename G, int NV, bool BLOCK, Mode MODE, bool RAGGED>
+__global__ void __launch_bounds__(BLOCK ? 1024 : 128) rows_kernel(NormArgs a, int tpr) {
+  constexpr int VEC = 16 / (int)sizeof(T), P = VEC / 2;
+  __shared__ Red red;
+  Lay<VEC, RAGGED> l;
+  l.tpr = BLOCK ? blockDim.x : tpr;
+  l.tid = BLOCK ? threadIdx.x : (threadIdx.x & (tpr - 1));
+  l.cols = a.cols;
+  const int per = BLOCK ? 1 : 128 / tpr;  // rows a block
+  int buf = 0;
+  for (int64_t first = blockIdx.x * (int64_t)per; first < a.rows; first += gridDim.x * (int64_t)per) {
+    int64_t row = first + (BLOCK ? 0 : threadIdx.x / tpr);
+    // lanes past the last row take part in the warp's steps with no columns
+    l.cols = row < a.rows ? a.cols : 0;
+    if (!BLOCK && row >= a.rows) row = a.rows - 1;
+    const T *x = static_cast<const T *>(a.x) + row * a.xs;
+    const T *r = static_cast<const T *>(a.residual) + row * a.rs;
+    l.m = shift_of<T, VEC>(x);
+    float2 h[NV][P];
+    Pack<G, VEC> g[NV];
+    {
+      Pack<T, VEC> px[NV], pr[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        px[i] = load_group(x, l, i);
+        if (MODE != kQuant && a.residual) pr[i] = load_group(r, l, i);
+        if (MODE != kQuant && a.gain) g[i] = load_gain(static_cast<const G *>(a.gain), l, i);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          h[i][p] = get2(px[i], p);
+          if (MODE != kQuant && a.residual) h[i][p] = add2(h[i][p], get2(pr[i], p));
+        }
+    }
+    finish_row<T, G, NV, BLOCK, MODE, RAGGED>(a, row, l, h, g, red, buf, [] {});
+  }
+}
+
+// Many rows, each on whole 16-byte groups: persistent blocks, a row a block,
+// each with a ring of row slots in shared memory that bulk copies fill ahead of
+// the row in work, so the reads of the next rows are in flight while a row is
+// reduced and written; the gains stay in registers.  (Straight loads wait out
+// each row's latency: 16384 rows of 8192 bf16 values with a residual took 259
+// us from rows_kernel, 173 us = 6.2 TB/s from here; 8192 x 4096 to 8 bits 71
+// and 47 us.)  A slot holds x's row, then the residual's.
+struct Ring {
+  int slots;
+  int row_bytes;   // one operand
+  int slot_bytes;  // both
+};
+constexpr int kMaxSlots = 3;
+
+template <typename T, typename G, int NV, Mode MODE>
+__global__ void __launch_bounds__(512)
+stream_rows_kernel(NormArgs a, Ring ring, int *status, long long wait_limit) {
+  constexpr int VEC = 16 / (int)sizeof(T), P = VEC / 2;
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ Red red;
+  __shared__ uint64_t bars[kMaxSlots];
+  Lay<VEC, false> l;
+  l.tpr = blockDim.x;
+  l.tid = threadIdx.x;
+  l.m = 0;
+  l.cols = a.cols;
+  const int64_t step = gridDim.x;
+  const unsigned full = smem_u32(&bars[0]);
+  const bool residual = MODE != kQuant && a.residual;
+  auto fetch = [&](int64_t row, int slot) {  // one thread
+    const unsigned dst = smem_u32(ring_smem + slot * ring.slot_bytes), bar = full + 8 * slot;
+    mbar_arrive_tx(bar, (unsigned)ring.slot_bytes);
+    bulk_load(dst, reinterpret_cast<uintptr_t>(static_cast<const T *>(a.x) + row * a.xs),
+              (unsigned)ring.row_bytes, bar);
+    if (residual)
+      bulk_load(dst + ring.row_bytes,
+                reinterpret_cast<uintptr_t>(static_cast<const T *>(a.residual) + row * a.rs),
+                (unsigned)ring.row_bytes, bar);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ring.slots; ++s) mbar_init(full + 8 * s, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    for (int s = 0; s < ring.slots; ++s)
+      if (blockIdx.x + s * step < a.rows) fetch(blockIdx.x + s * step, s);
+  }
+  Pack<G, VEC> g[NV];
+  if (MODE != kQuant && a.gain) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) g[i] = load_gain(static_cast<const G *>(a.gain), l, i);
+  }
+  __syncthreads();
+  int buf = 0, slot = 0;
+  unsigned parity = 0;
+  long long limit = wait_limit;
+  for (int64_t row = blockIdx.x; row < a.rows; row += step) {
+    // A wait that runs out is reported and the copy drained (with its own
+    // bound); later waits then only look once.
+    bool ok = false;
+    for (long long it = 0; it < limit && !ok; ++it) ok = mbar_try_wait(full + 8 * slot, parity);
+    if (!ok) {
+      if (status) atomicExch(status, 401);
+      mbar_drain(full + 8 * slot, parity);
+      limit = 1;
+    }
+    const unsigned char *at = ring_smem + slot * ring.slot_bytes;
+    auto take = [&](int off, int i) {
+      Pack<T, VEC> p;
+      if (l.whole(i)) {
+        p = *reinterpret_cast<const Pack<T, VEC> *>(at + off + 16 * (l.tid + i * l.tpr));
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) p.v[e] = from_f32<T>(0.0f);
+      }
+      return p;
+    };
+    float2 h[NV][P];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Pack<T, VEC> px = take(0, i);
+#pragma unroll
+      for (int p = 0; p < P; ++p) h[i][p] = get2(px, p);
+      if (residual) {
+        const Pack<T, VEC> pr = take(ring.row_bytes, i);
+#pragma unroll
+        for (int p = 0; p < P; ++p) h[i][p] = add2(h[i][p], get2(pr, p));
+      }
+    }
+    const int64_t next = row + ring.slots * step;
+    finish_row<T, G, NV, true, MODE, false>(a, row, l, h, g, red, buf, [&] {
+      if (threadIdx.x == 0 && next < a.rows) fetch(next, slot);
+    });
+    if (++slot == ring.slots) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+}
+
+// Rows longer than a block's registers, and tensors whose rows do not start
+// alike: one block a row, value by value, read twice (the second time mostly
+// from L2).  The sum is written on the second read, by the thread that read its
+// operands, so it may be x or the residual.
+template <typename T, typename G, Mode MODE>
 __global__ void __launch_bounds__(1024) long_rows_kernel(NormArgs a) {
   __shared__ Red red;
   int buf = 0;
   const G *gain = static_cast<const G *>(a.gain);
+  const int n = blockDim.x;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T *x = static_cast<const T *>(a.x) + row * a.xs;
     const T *r = static_cast<const T *>(a.residual) + row * a.rs;
     auto h_of = [&](int c) {
       float h = to_f32(x[c]);
-      if (NORM && a.residual) h += to_f32(r[c]);
+      if (MODE != kQuant && a.residual) h += to_f32(r[c]);
       return h;
     };
     auto t_of = [&](float h, int c) {
-      return NORM && gain ? __fmul_rn(h, to_f32(gain[c])) : h;
+      return MODE != kQuant && gain ? __fmul_rn(h, to_f32(gain[c])) : h;
     };
-    float s = 0.0f;
-    unsigned m = 0, hm = 0;
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    float s = 0.0f, top = 0.0f, hm = 0.0f;
+    for (int c = threadIdx.x; c < a.cols; c += n) {
       const float h = h_of(c);
       s = fmaf(h, h, s);
-      hm = max(hm, abs_bits(h));
-      m = max(m, abs_bits(t_of(h, c)));
+      hm = max_abs(hm, h, 0.0f);
+      top = max_abs(top, t_of(h, c), 0.0f);
     }
-    reduce_row<true>(s, m, red, buf);
+    reduce_row<true>(s, top, red, buf, n);
     float rstd = 1.0f;
-    if (NORM) {
+    if (MODE != kQuant) {
       rstd = row_rstd(s, a.cols, a.eps);
-      if (!(s < __uint_as_float(kInfBits))) {  // as in rows_kernel
-        float s2 = 0.0f;
-        reduce_row<true>(s2, hm, red, buf);
-        if (hm < kInfBits) {
-          const float down = pow2(167 - (int)(hm >> 23));
-          s2 = 0.0f;
-          for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+      if (!(s < __uint_as_float(kInfBits))) {  // as in finish_row
+        float zero = 0.0f, none = 0.0f;
+        reduce_row<true>(zero, hm, red, buf, n);
+        if (hm < __uint_as_float(kInfBits)) {
+          const float down = pow2(167 - (int)(__float_as_uint(hm) >> 23));
+          float d = 0.0f;
+          for (int c = threadIdx.x; c < a.cols; c += n) {
             const float h = h_of(c) * down;
-            s2 = fmaf(h, h, s2);
+            d = fmaf(h, h, d);
           }
-          unsigned none = 0;
-          reduce_row<true>(s2, none, red, buf);
-          rstd = row_rstd(s2, a.cols, a.eps * down * down) * down;
+          reduce_row<true>(d, none, red, buf, n);
+          rstd = row_rstd(d, a.cols, a.eps * down * down) * down;
         }
       }
     }
-    const Quant z = a.q ? make_quant(m, rstd) : Quant{1.0f, 0.0f, 0.0f};
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    const Quant z = MODE != kNorm ? make_quant(top, rstd) : Quant{1.0f, 0.0f, 0.0f};
+    for (int c = threadIdx.x; c < a.cols; c += n) {
       const float h = h_of(c);
-      if (NORM && a.sum) static_cast<T *>(a.sum)[row * a.ss + c] = from_f32<T>(h);
-      if (NORM && a.y) {
+      if (MODE != kQuant && a.sum) static_cast<T *>(a.sum)[row * a.ss + c] = from_f32<T>(h);
+      if constexpr (MODE == kNorm) {
         float v = h * rstd;
         if (gain) v *= to_f32(gain[c]);
         static_cast<T *>(a.y)[row * a.ys + c] = from_f32<T>(v);
+      } else {
+        const float2 t[2] = {make_float2(t_of(h, c), 0.0f), both(0.0f)};
+        a.q[row * a.qs + c] = (int8_t)quantise(t, z);
       }
-      if (a.q) a.q[row * a.qs + c] = quantise(t_of(h, c), z);
     }
-    if (a.q && threadIdx.x == 0) a.scale[row] = z.scale;
+    if (MODE != kNorm && threadIdx.x == 0) a.scale[row] = z.scale;
   }
 }
 
-template <typename T, typename G, int VEC, int NV, bool NORM>
-void launch_nv(const NormArgs &a, int groups, cudaStream_t st) {
-  constexpr int64_t kMaxGrid = 0x7fffffff;
-  if (groups <= 32 * NV) {
-    const int64_t blocks = (a.rows + 3) / 4;
-    rows_kernel<T, G, VEC, NV, false, NORM>
-        <<<(unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid), 128, 0, st>>>(a);
-  } else {
-    const int threads = ((groups + NV - 1) / NV + 31) / 32 * 32;
-    rows_kernel<T, G, VEC, NV, true, NORM>
-        <<<(unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid), threads, 0, st>>>(a);
-  }
+int up32(int v) { return (v + 31) / 32 * 32; }
+
+constexpr int kSms = 148;
+constexpr int kMaxGroups = 4096;  // 16-byte groups a row that a block's registers hold
+
+template <typename T, typename G, int NV, Mode MODE>
+bv_status launch_stream(const NormArgs &a, int threads, cudaStream_t st) {
+  // Blocks an SM: 1024 threads' worth (8192 x 2048 bf16 to 8 bits: 27.3 us so,
+  // 28.0 us with half of them).  Past 256 threads one block with a residual
+  // (16384 x 8192 bf16 173 us, two blocks 194 us), else two (8192 x 8192 f32 to
+  // 8 bits 53 us, one block 61 us).
+  Ring ring;
+  ring.row_bytes = a.cols * (int)sizeof(T);
+  ring.slot_bytes = ring.row_bytes * (a.residual ? 2 : 1);
+  int per_sm = threads <= 256 ? 1024 / threads : a.residual ? 1 : 2;
+  per_sm = std::max(1, std::min(per_sm, 200 * 1024 / (2 * ring.slot_bytes)));
+  ring.slots = std::min(per_sm == 1 ? 3 : 2, 216 * 1024 / ring.slot_bytes);  // 1 past 108 KB
+  int *status = device_status_ptr();
+  if (!status) return fail(BV_ERR_CUDA, "rms_norm: status word");
+  const size_t smem = (size_t)ring.slots * ring.slot_bytes;
+  auto k = stream_rows_kernel<T, G, NV, MODE>;
+  // (room beside the kernel's static shared memory too)
+  BV_TRY(ensure_dynamic_smem((const void *)k, smem + 2048, "rms_norm smem"));
+  const int64_t blocks = std::min<int64_t>(a.rows, kSms * per_sm);
+  k<<<(unsigned)blocks, threads, smem, st>>>(a, ring, status, wait_limit());
+  return BV_OK;
 }
 
-template <typename T, typename G, bool NORM>
-void launch_typed(const NormArgs &a, cudaStream_t st) {
+template <typename T, typename G, int NV, bool BLOCK, Mode MODE, bool RAGGED>
+bv_status launch_direct(const NormArgs &a, int threads, cudaStream_t st) {
+  const int per = BLOCK ? 1 : 128 / threads;
+  const int64_t blocks = std::min<int64_t>((a.rows + per - 1) / per, 0x7fffffff);
+  rows_kernel<T, G, NV, BLOCK, MODE, RAGGED>
+      <<<(unsigned)blocks, BLOCK ? threads : 128, 0, st>>>(a, threads);
+  return BV_OK;
+}
+
+// Which kernel, and how many of a row's groups a thread takes.
+template <typename T, typename G, Mode MODE, bool RAGGED>
+bv_status launch_vec(const NormArgs &a, cudaStream_t st) {
   constexpr int VEC = 16 / (int)sizeof(T);
-  auto vec_rows = [&](const void *p, int64_t stride, int esize) {
+  const int groups = (a.cols + (RAGGED ? VEC - 1 : 0) + VEC - 1) / VEC;
+  // Short rows: the fewest lanes with two groups each (65536 rows of 64 f32
+  // values: 8.7 us with 8 lanes of two groups, 10.2 us with 16 of one).
+  if (groups <= 64) {
+    int lanes = 4;
+    while (2 * lanes < groups) lanes *= 2;
+    return launch_direct<T, G, 2, false, MODE, RAGGED>(a, lanes, st);
+  }
+  // Two blocks an SM and more go through the ring (300 x 4096 bf16 to 8 bits:
+  // 5.3 us, 5.7 us without it; 1200 x 4096: 9.7 and 13.8 us).  Ragged rows
+  // spend their time at the rows' ends, ring or not (8192 x 1501 bf16 to 8
+  // bits: 47 us through one, 40 us without).
+  const bool many = a.rows >= 2 * kSms;
+  if constexpr (!RAGGED) {
+    if (many) {
+      if (groups <= 1024) return launch_stream<T, G, 2, MODE>(a, up32((groups + 1) / 2), st);
+      if (groups <= 2048) return launch_stream<T, G, 4, MODE>(a, up32((groups + 3) / 4), st);
+      return launch_stream<T, G, 8, MODE>(a, up32((groups + 7) / 8), st);
+    }
+  }
+  // Few rows: one group a thread, as long as a block has threads (one row of
+  // 4096 bf16 values: 2.6 us with 512 threads, 3.0 us with 256).
+  if (!many && groups <= 1024) return launch_direct<T, G, 1, true, MODE, RAGGED>(a, up32(groups), st);
+  if (groups <= (many ? 1024 : 2048))
+    return launch_direct<T, G, 2, true, MODE, RAGGED>(a, up32((groups + 1) / 2), st);
+  return launch_direct<T, G, 4, true, MODE, RAGGED>(a, up32((groups + 3) / 4), st);
+}
+
+template <typename T, typename G, Mode MODE>
+bv_status launch_typed(const NormArgs &a, cudaStream_t st) {
+  constexpr int VEC = 16 / (int)sizeof(T);
+  // a tensor's rows start on whole groups (its elements' alignment is given)
+  auto starts = [&](const void *p, int64_t stride, int esize) {
     return !p || (aligned_to(p, VEC * esize) && (stride % VEC == 0 || a.rows <= 1));
   };
-  const bool vec = vec_rows(a.x, a.xs, sizeof(T)) && vec_rows(a.residual, a.rs, sizeof(T)) &&
-                   vec_rows(a.sum, a.ss, sizeof(T)) && vec_rows(a.y, a.ys, sizeof(T)) &&
-                   vec_rows(a.q, a.qs, 1) && vec_rows(a.gain, 0, sizeof(G) < 4 ? 2 : 4);
-  if (vec) {
-    const int groups = (a.cols + VEC - 1) / VEC;
-    if (groups <= 256) launch_nv<T, G, VEC, 1, NORM>(a, groups, st);
-    else if (groups <= 512) launch_nv<T, G, VEC, 2, NORM>(a, groups, st);
-    else if (groups <= 4096) launch_nv<T, G, VEC, 4, NORM>(a, groups, st);
-  } else {
-    if (a.cols <= 1024) launch_nv<T, G, 1, 4, NORM>(a, a.cols, st);
-    else if (a.cols <= 16384) launch_nv<T, G, 1, 16, NORM>(a, a.cols, st);
-  }
-  if (vec ? (a.cols + VEC - 1) / VEC > 4096 : a.cols > 16384) {
-    const int64_t grid = a.rows < 0x7fffffff ? a.rows : 0x7fffffff;
-    long_rows_kernel<T, G, NORM><<<(unsigned)grid, 1024, 0, st>>>(a);
-  }
+  // rows as far past a group's start as x's, each of them
+  auto follows = [&](const void *p, int64_t stride) {
+    return !p || (((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(a.x)) % 16 == 0) &&
+                  ((stride - a.xs) % VEC == 0 || a.rows <= 1));
+  };
+  constexpr int es = (int)sizeof(T);
+  const bool fits = (a.cols + 2 * VEC - 2) / VEC <= kMaxGroups && starts(a.q, a.qs, 1);
+  if (fits && a.cols % VEC == 0 && starts(a.x, a.xs, es) && starts(a.residual, a.rs, es) &&
+      starts(a.sum, a.ss, es) && starts(a.y, a.ys, es) && starts(a.gain, 0, (int)sizeof(G)))
+    return launch_vec<T, G, MODE, false>(a, st);
+  if (fits && follows(a.residual, a.rs) && follows(a.sum, a.ss) && follows(a.y, a.ys))
+    return launch_vec<T, G, MODE, true>(a, st);
+  const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 0x7fffffff);
+  long_rows_kernel<T, G, MODE><<<grid, std::min(1024, up32((a.cols + 3) / 4)), 0, st>>>(a);
+  return BV_OK;
+}
+
+template <typename T, typename G>
+bv_status launch_norm(const NormArgs &a, cudaStream_t st) {
+  return a.q ? launch_typed<T, G, kNorm8>(a, st) : launch_typed<T, G, kNorm>(a, st);
 }
 
 // Row offsets of a tensor stay far inside 64 bits.
@@ -376,15 +701,15 @@ bv_status launch_rows(const NormArgs &a, int dtype, int gain_dtype, cudaStream_t
     LaunchTimer tm(st, a.norm ? "rms_norm" : "quantize_rows", (a.norm ? 6.0 : 3.0) * n, bytes);
     if (a.norm) {
       const bool f32g = gain_dtype == BV_F32;
-      if (dtype == BV_F32) launch_typed<float, float, true>(a, st);
-      else if (dtype == BV_BF16 && f32g) launch_typed<__nv_bfloat16, float, true>(a, st);
-      else if (dtype == BV_BF16) launch_typed<__nv_bfloat16, __nv_bfloat16, true>(a, st);
-      else if (f32g) launch_typed<__half, float, true>(a, st);
-      else launch_typed<__half, __half, true>(a, st);
+      if (dtype == BV_F32) BV_TRY((launch_norm<float, float>(a, st)));
+      else if (dtype == BV_BF16 && f32g) BV_TRY((launch_norm<__nv_bfloat16, float>(a, st)));
+      else if (dtype == BV_BF16) BV_TRY((launch_norm<__nv_bfloat16, __nv_bfloat16>(a, st)));
+      else if (f32g) BV_TRY((launch_norm<__half, float>(a, st)));
+      else BV_TRY((launch_norm<__half, __half>(a, st)));
     } else {
-      if (dtype == BV_F32) launch_typed<float, float, false>(a, st);
-      else if (dtype == BV_BF16) launch_typed<__nv_bfloat16, __nv_bfloat16, false>(a, st);
-      else launch_typed<__half, __half, false>(a, st);
+      if (dtype == BV_F32) BV_TRY((launch_typed<float, float, kQuant>(a, st)));
+      else if (dtype == BV_BF16) BV_TRY((launch_typed<__nv_bfloat16, __nv_bfloat16, kQuant>(a, st)));
+      else BV_TRY((launch_typed<__half, __half, kQuant>(a, st)));
     }
   }
   count_launch();

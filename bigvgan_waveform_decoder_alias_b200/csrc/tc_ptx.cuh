@@ -143,6 +143,15 @@ __device__ __forceinline__ void tma_load_2d_pair(unsigned dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar & kPeerBitMask)
       : "memory");
 }
+// `bytes` (a multiple of 16) from global `src` (16-byte aligned) to this CTA's
+// shared memory, counted by the barrier.
+__device__ __forceinline__ void bulk_load(unsigned dst, uintptr_t src, unsigned bytes, unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+          dst),
+      "l"((uint64_t)src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 // Arrive on the barrier at this offset in both CTAs once the MMAs issued so
 // far have completed.
 __device__ __forceinline__ void mma_commit_pair(unsigned bar) {

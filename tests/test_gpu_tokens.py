@@ -83,7 +83,10 @@ def expected_q(x, residual, gain):
 
 SIZES = [(1, 1), (1, 8), (3, 7), (2, 32), (5, 127), (4, 128), (3, 255), (2, 1000), (7, 1024),
          (1, 1537), (3, 2048), (2, 2056), (5, 4096), (1, 8192), (2, 8200), (3, 11000),
-         (1, 16384), (2, 16392), (1, 20001), (2, 32768), (1, 32776), (2, 70000)]
+         (1, 16384), (2, 16392), (1, 20001), (2, 32768), (1, 32776), (2, 70000),
+         # enough rows for every SM: through the ring of the persistent kernel
+         (1000, 24), (301, 512), (700, 520), (1300, 1024), (299, 1537), (333, 2048), (900, 4096),
+         (600, 8192), (297, 16384), (450, 32768)]
 
 
 @pytest.mark.parametrize("dtype", ALL)
