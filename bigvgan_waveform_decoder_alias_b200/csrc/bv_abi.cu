@@ -33,8 +33,17 @@ std::atomic<long long> g_wait_limit{kDefaultWaitLimit};
 long long wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
 
 int *device_status_ptr() {
+  // looked up once a device (the lookup costs more than a small launch's checks)
+  constexpr int kMaxDev = 64;
+  static std::atomic<int *> cache[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  const bool slot = dev >= 0 && dev < kMaxDev;
+  if (slot)
+    if (int *hit = cache[dev].load(std::memory_order_relaxed)) return hit;
   void *p = nullptr;
   if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return nullptr;
+  if (slot) cache[dev].store(static_cast<int *>(p), std::memory_order_relaxed);
   return static_cast<int *>(p);
 }
 

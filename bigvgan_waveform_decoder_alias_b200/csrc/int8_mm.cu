@@ -80,16 +80,21 @@ __device__ __forceinline__ void tmem_wait_ld() {
 
 __device__ __forceinline__ unsigned bits16(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 __device__ __forceinline__ unsigned bits16(__half v) { return __half_as_ushort(v); }
-__device__ __forceinline__ unsigned bits16(float) { return 0; }
+[[maybe_unused]] __device__ __forceinline__ unsigned bits16(float) { return 0; }
 
 // The residual of a warp's 32 rows (row0 + lane) x N columns from col0 on.
 template <typename T, int N>
 __device__ __forceinline__ void load_residual(const Mm &p, int row0, int lane, int col0, T (&r)[N]) {
   if (!p.residual || row0 + lane >= p.rows) return;
   const T *res = static_cast<const T *>(p.residual) + (int64_t)col0 * p.rs + row0 + lane;
+  if (col0 + N <= p.cols) {
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (col0 + e < p.cols) r[e] = res[e * p.rs];
+    for (int e = 0; e < N; ++e) r[e] = res[e * p.rs];
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (col0 + e < p.cols) r[e] = res[e * p.rs];
+  }
 }
 
 // Those columns of the accumulator go out: `rscale`, `rbias` are this lane's
@@ -99,6 +104,35 @@ __device__ __forceinline__ void load_residual(const Mm &p, int row0, int lane, i
 // A 16-bit column is half a word a lane, so lanes swap halves in pairs: the
 // even one writes two rows of the even column, the odd one two rows of the odd
 // column.
+// WHOLE: 32 rows and N columns in range (and, of 16-bit outputs, `pairs`); this
+// form has no branch, so that the columns' steps overlap (with branches between
+// them a warp took some 250 cycles a pair, and the epilogue of 4800 x 4096 x
+// 1024 four times the products' time).
+template <typename T, int N, bool WHOLE, bool RESIDUAL>
+__device__ __forceinline__ void write_columns(const Mm &p, const int (&acc)[N], int row, int lane,
+                                              int col0, int nc, float rscale, float rbias,
+                                              const float *cs, const float *cb, const T (&r)[N]) {
+  constexpr bool PAIRS = WHOLE && sizeof(T) == 2;
+  const int odd = PAIRS ? lane & 1 : 0;
+  const bool in = row < p.rows;
+  T *y = static_cast<T *>(p.y) + (int64_t)(col0 + odd) * p.ys + (row - odd);
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    const float2 s = mul2(*reinterpret_cast<const float2 *>(cs + e), both(rscale));
+    const float2 b = add2(*reinterpret_cast<const float2 *>(cb + e), both(rbias));
+    float2 f = fma2(make_float2((float)acc[e], (float)acc[e + 1]), s, b);
+    if constexpr (RESIDUAL) f = add2(f, make_float2(to_f32(r[e]), to_f32(r[e + 1])));
+    if constexpr (PAIRS) {
+      const unsigned v0 = bits16(from_f32<T>(f.x)), v1 = bits16(from_f32<T>(f.y));
+      const unsigned got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+      *reinterpret_cast<unsigned *>(y + e * p.ys) = odd ? __byte_perm(got, v1, 0x5410)
+                                                        : __byte_perm(v0, got, 0x5410);
+    } else {
+      if (WHOLE || (in && e < nc)) y[e * p.ys] = from_f32<T>(f.x);
+      if (WHOLE || (in && e + 1 < nc)) y[(e + 1) * p.ys] = from_f32<T>(f.y);
+    }
+  }
+}
 template <typename T, int N>
 __device__ __forceinline__ void store_columns(const Mm &p, const int (&acc)[N], int row0, int lane,
                                               int col0, float rscale, float rbias, const float *cs,
@@ -106,27 +140,13 @@ __device__ __forceinline__ void store_columns(const Mm &p, const int (&acc)[N], 
   static_assert(N % 2 == 0, "columns go out in pairs");
   const int nc = min(N, p.cols - col0);  // warp-uniform
   if (row0 >= p.rows || nc <= 0) return;
-  const int row = row0 + lane;
-  const bool in = row < p.rows;
-  const bool pairs = sizeof(T) == 2 && p.pairs && row0 + 32 <= p.rows;
-  const int odd = pairs ? lane & 1 : 0;
-  T *y = static_cast<T *>(p.y) + (int64_t)(col0 + odd) * p.ys + (row - odd);
-#pragma unroll
-  for (int e = 0; e < N; e += 2, y += 2 * p.ys) {
-    const float2 s = mul2(*reinterpret_cast<const float2 *>(cs + e), both(rscale));
-    const float2 b = add2(*reinterpret_cast<const float2 *>(cb + e), both(rbias));
-    float2 f = fma2(make_float2((float)acc[e], (float)acc[e + 1]), s, b);
-    if (p.residual) f = add2(f, make_float2(to_f32(r[e]), to_f32(r[e + 1])));
-    if (pairs) {
-      T v[2] = {from_f32<T>(f.x), from_f32<T>(f.y)};
-      const unsigned give = odd ? bits16(v[0]) : bits16(v[1]);
-      const unsigned got = __shfl_xor_sync(0xffffffffu, give, 1);
-      const unsigned word = odd ? (got | (bits16(v[1]) << 16)) : (bits16(v[0]) | (got << 16));
-      if (e + odd < nc) *reinterpret_cast<unsigned *>(y) = word;
-    } else if (in) {
-      if (e < nc) y[0] = from_f32<T>(f.x);
-      if (e + 1 < nc) y[p.ys] = from_f32<T>(f.y);
-    }
+  const bool whole = nc == N && row0 + 32 <= p.rows && (sizeof(T) == 4 || p.pairs);
+  if (p.residual) {
+    if (whole) write_columns<T, N, true, true>(p, acc, row0 + lane, lane, col0, nc, rscale, rbias, cs, cb, r);
+    else write_columns<T, N, false, true>(p, acc, row0 + lane, lane, col0, nc, rscale, rbias, cs, cb, r);
+  } else {
+    if (whole) write_columns<T, N, true, false>(p, acc, row0 + lane, lane, col0, nc, rscale, rbias, cs, cb, r);
+    else write_columns<T, N, false, false>(p, acc, row0 + lane, lane, col0, nc, rscale, rbias, cs, cb, r);
   }
 }
 
@@ -136,25 +156,6 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
 
 __host__ __device__ constexpr int tmem_cols(int n) {
   return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512;
-}
-
-// ------------------------------------------------------- few columns or tiles
-//
-// One CTA a tile of 128 rows x NT columns, or a cluster of up to eight CTAs
-// that take a share of K each: with few tokens the weight's bytes bound the
-// product, and only a split over K gives every SM some of them.  The shares
-// are joined through distributed shared memory: each CTA leaves its partial
-// sums in its own, then sums and writes the columns col % split = rank.
-// Integers, so the join's order does not show.
-//
-// TMA: thread 0 loads the stages by TMA.  Otherwise (rows that do not start on
-// 16 bytes) warps 4..7 copy them: aligned words, shifted into place.
-
-constexpr int TILE_MAX_STAGES = 12;
-
-template <int NT>
-constexpr int tile_stage_bytes() {
-  return (BR + NT) * BK;
 }
 
 // 16 bytes of K from byte k on of a row, zero past K.  Aligned words are
@@ -189,6 +190,94 @@ __device__ __forceinline__ uint4 load16(const int8_t *row, int k, int K, const i
     if (left < 4) v[i] = left <= 0 ? 0u : v[i] & (0xffffffffu >> (32 - 8 * left));
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// ------------------------------------------------------------- few columns
+//
+// One to four columns (single tokens): bound by the rows' bytes, each read
+// once, so the dot products stay on the CUDA cores (four products an
+// instruction) and nothing is staged.  A block takes R rows and all of K: a
+// thread reads 16 bytes of each row and column at a time, 128 threads apart.
+
+constexpr int DOT_THREADS = 128;
+
+template <typename T, int R, int C>
+__global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p, bool aligned) {
+  __shared__ int part[DOT_THREADS / 32][R * C];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = (int)blockIdx.x * R;
+  const int8_t *rhi = p.r + (int64_t)(p.rows - 1) * p.rstride + p.K;
+  const int8_t *chi = p.c + (int64_t)(p.cols - 1) * p.cstride + p.K;
+  int acc[R][C] = {};
+  for (int k = 16 * threadIdx.x; k < p.K; k += 16 * DOT_THREADS) {
+    uint4 r[R], c[C];
+    const bool whole = aligned && k + 16 <= p.K;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int8_t *row = p.r + (int64_t)min(row0 + i, p.rows - 1) * p.rstride;
+      r[i] = whole ? __ldg(reinterpret_cast<const uint4 *>(row + k)) : load16(row, k, p.K, p.r, rhi);
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int8_t *col = p.c + (int64_t)min(j, p.cols - 1) * p.cstride;
+      c[j] = whole ? __ldg(reinterpret_cast<const uint4 *>(col + k)) : load16(col, k, p.K, p.c, chi);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        int s = acc[i][j];
+        s = __dp4a((int)r[i].x, (int)c[j].x, s);
+        s = __dp4a((int)r[i].y, (int)c[j].y, s);
+        s = __dp4a((int)r[i].z, (int)c[j].z, s);
+        acc[i][j] = __dp4a((int)r[i].w, (int)c[j].w, s);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int s = __reduce_add_sync(0xffffffffu, acc[i][j]);
+      if (lane == 0) part[warp][i * C + j] = s;
+    }
+  // what the epilogue reads, on its way to the barrier
+  const int i = threadIdx.x / C, j = threadIdx.x % C, row = row0 + i;
+  const bool mine = threadIdx.x < R * C && row < p.rows && j < p.cols;
+  float s = 0.0f, b = 0.0f, res = 0.0f;
+  if (mine) {
+    s = __fmul_rn(__ldg(p.c_scale + j), __ldg(p.r_scale + row));
+    b = p.r_bias ? __ldg(p.r_bias + row) : p.c_bias ? __ldg(p.c_bias + j) : 0.0f;
+    if (p.residual) res = to_f32(static_cast<const T *>(p.residual)[j * p.rs + row]);
+  }
+  __syncthreads();
+  if (mine) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < DOT_THREADS / 32; ++w) sum += part[w][i * C + j];
+    float f = fmaf((float)sum, s, b);
+    if (p.residual) f += res;
+    static_cast<T *>(p.y)[j * p.ys + row] = from_f32<T>(f);
+  }
+}
+
+// ------------------------------------------------------------- few tiles
+//
+// One CTA a tile of 128 rows x NT columns, or a cluster of up to eight CTAs
+// that take a share of K each: with few tokens the weight's bytes bound the
+// product, and only a split over K gives every SM some of them.  The shares
+// are joined through distributed shared memory: each CTA leaves its partial
+// sums in its own, then sums and writes NT / split of the columns.  Integers, so
+// the join's order does not show.  (Adding to the owner's shared memory from
+// afar instead took longer: 16 x 8192 x 2048 11.2 us, 10.0 us so.)
+//
+// TMA: thread 0 loads the stages by TMA.  Otherwise (rows that do not start on
+// 16 bytes) warps 4..7 copy them: aligned words, shifted into place.
+
+constexpr int TILE_MAX_STAGES = 12;
+
+template <int NT>
+constexpr int tile_stage_bytes() {
+  return (BR + NT) * BK;
 }
 
 template <typename T, int NT, bool TMA>
@@ -394,13 +483,13 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
 //
 // Persistent CTA pairs: a pair's tile is 256 rows x NT columns (cta_group::2:
 // each CTA holds half of the rows and loads half of the columns), TMA fills a
-// ring of stages, and two accumulators of NT columns in TMEM let eight warps a
+// ring of stages, and two accumulators of NT columns in TMEM let sixteen warps a
 // CTA write one tile out while the tensor cores work on the next.  Tiles are
 // walked in bands of BAND row tiles, so that the pairs at work at one time share
 // operand tiles in L2.
 
-constexpr int PAIR_THREADS = 384;
-constexpr int PAIR_EPI_WARPS = 8;
+constexpr int PAIR_EPI_WARPS = 16;  // of a CTA: four for each 32 rows
+constexpr int PAIR_THREADS = 128 + 32 * PAIR_EPI_WARPS;
 constexpr int BAND = 8;
 
 template <int NT>
@@ -539,7 +628,7 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
       mbar_drain(bar_done, 0);
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., half of the columns
+    const int q = warp & 3, part = (warp - 4) >> 2;  // TMEM lanes 32 q .., a quarter of the columns
     const int ct = threadIdx.x - 128;                // column whose scale this thread fetches
     const unsigned free_leader = map_to_rank(bar_free, 0);
     // a tile's scales and biases are fetched while the tile before it goes out
@@ -557,9 +646,6 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
     };
     fetch(pid);
     int it = 0;
-    // after a wait that gave up the warp still takes every barrier, and writes
-    // nothing
-    bool alive = true;
     for (int tau = pid; tau < n_tiles; tau += pairs, ++it) {
       int row0, col0;
       tile_at(tau, row0, col0);
@@ -571,30 +657,28 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
         cb[buf][ct] = n_cb;
       }
       fetch(tau + pairs);
-      asm volatile("bar.sync 1, 256;\n" ::: "memory");  // cs, cb of this tile
-      const int c0 = half * (NT / 2);
-      T r[2][16];
-      load_residual(p, row0, lane, col0 + c0, r[0]);
-      if (!warp_wait(bar_acc + 8 * buf, (it >> 1) & 1, wc, 314)) alive = false;
+      const int c0 = part * (NT / 4);
+      T r[16];
+      load_residual(p, row0, lane, col0 + c0, r);
+      // one warp waits for the sums; the barrier hands that on, and cs and cb
+      if (warp == 4) warp_wait(bar_acc + 8 * buf, (it >> 1) & 1, wc, 314);
+      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * PAIR_EPI_WARPS) : "memory");
       asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
       const unsigned acc = tmem + ((unsigned)(32 * q) << 16) + (unsigned)(buf * NT + c0);
-      int v[2][16];
-      tmem_ld16(acc, v[0]);
 #pragma unroll
-      for (int c = 0; c < NT / 2; c += 16) {
-        const int now = (c >> 4) & 1, next = now ^ 1;
+      for (int c = 0; c < NT / 4; c += 16) {
+        int v[16];
+        tmem_ld16(acc + c, v);
         tmem_wait_ld();
-        if (c + 16 < NT / 2) {
-          tmem_ld16(acc + c + 16, v[next]);
-          load_residual(p, row0, lane, col0 + c0 + c + 16, r[next]);
-        } else {
+        if (c + 16 == NT / 4) {
           asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
           __syncwarp();
           if (lane == 0) arrive_remote(free_leader + 8 * buf);
         }
-        if (alive)
-          store_columns(p, v[now], row0, lane, col0 + c0 + c, rscale, rbias, cs[buf] + c0 + c,
-                        cb[buf] + c0 + c, r[now]);
+        if (!ctl.abort)  // after a wait that gave up nothing more is written
+          store_columns(p, v, row0, lane, col0 + c0 + c, rscale, rbias, cs[buf] + c0 + c,
+                        cb[buf] + c0 + c, r);
+        if (c + 16 < NT / 4) load_residual(p, row0, lane, col0 + c0 + c + 16, r);
       }
     }
   }
@@ -637,30 +721,21 @@ bv_status encode_rows(CUtensorMap *map, const int8_t *p, int64_t stride, int row
 }
 
 template <typename T, int NT, bool TMA>
-bv_status run_tile(const Mm &p, cudaStream_t st) {
+bv_status run_tile(const Mm &p, int split, cudaStream_t st) {
   const int64_t tiles_r = ((int64_t)p.rows + BR - 1) / BR, tiles_c = ((int64_t)p.cols + NT - 1) / NT;
   const int64_t tiles = tiles_r * tiles_c;
   const int chunks = (p.K + BK - 1) / BK;
-  int split = 1;
-#ifdef BV_INT8_SWEEP
-  split = sweep_split;
-  while (split > 1 && chunks < 2 * split) split /= 2;
-#else
-  while (split < MAX_SPLIT && tiles * split * 2 <= 296 && chunks >= 4 * split) split *= 2;
-#endif
   if (tiles * split > 0x7fffffff) return fail(BV_ERR_SHAPE, "bv_int8_matmul: grid");
   constexpr int STAGE = tile_stage_bytes<NT>();
   const int per = (chunks + split - 1) / split;
   // two CTAs an SM; room for the partial sums of a split tile
   int stages = std::min(std::min(per, TILE_MAX_STAGES), (112 * 1024 - 1024) / STAGE);
-#ifdef BV_INT8_SWEEP
-  stages = std::min(std::min(per, TILE_MAX_STAGES), (sweep_kb * 1024 - 1024) / STAGE);
-#endif
   const int least = split > 1 ? (NT * BR * 4 + STAGE - 1) / STAGE : 1;
   stages = std::max(stages, least);
   const size_t smem = (size_t)stages * STAGE + 1024;
   auto kernel = int8_tile_kernel<T, NT, TMA>;
-  BV_TRY(ensure_dynamic_smem((const void *)kernel, smem, "bv_int8_matmul smem"));
+  // (room beside the kernel's static shared memory too)
+  BV_TRY(ensure_dynamic_smem((const void *)kernel, smem + 2048, "bv_int8_matmul smem"));
   CUtensorMap mr{}, mc{};
   if (TMA) {
     BV_TRY(encode_rows(&mr, p.r, p.rstride, p.rows, p.K, BR));
@@ -704,25 +779,82 @@ bv_status run_pair(const Mm &p, cudaStream_t st) {
   return BV_OK;
 }
 
+template <typename T, int R, int C>
+bv_status run_dot(const Mm &p, bool aligned, cudaStream_t st) {
+  int8_dot_kernel<T, R, C><<<(unsigned)((p.rows + (int64_t)R - 1) / R), DOT_THREADS, 0, st>>>(p, aligned);
+  return BV_OK;
+}
+template <typename T, int C>
+bv_status run_dot_rows(const Mm &p, bool aligned, cudaStream_t st) {
+  // the most rows a block that leave three blocks an SM
+  const int blocks = 3 * 148;
+  if (p.rows >= 8 * blocks) return run_dot<T, 8, C>(p, aligned, st);
+  if (p.rows >= 4 * blocks) return run_dot<T, 4, C>(p, aligned, st);
+  if (p.rows >= 2 * blocks) return run_dot<T, 2, C>(p, aligned, st);
+  return run_dot<T, 1, C>(p, aligned, st);
+}
+template <typename T>
+bv_status run_dots(const Mm &p, bool aligned, cudaStream_t st) {
+  if (p.cols == 1) return run_dot_rows<T, 1>(p, aligned, st);
+  if (p.cols == 2) return run_dot_rows<T, 2>(p, aligned, st);
+  return run_dot_rows<T, 4>(p, aligned, st);
+}
+
+int64_t tile_count(const Mm &p, int rows, int cols) {
+  return (((int64_t)p.rows + rows - 1) / rows) * (((int64_t)p.cols + cols - 1) / cols);
+}
+
+// Columns of a pair's tile, or 0 where there are too few tiles to go round.  A
+// wave of tiles takes about as long as its operands take from L2, which is as
+// 256 + NT; e.g. 512 x 4096 x 4096: 17.7 us with 128 columns (one wave), 28.1 us with
+// 64 (two), 19.2 us with 256 (one).  From 60 tiles of 64 columns on the pairs win
+// (256 x 4096 x 4096 16.7 us, 16.9 us in few tiles; 128 x 4096 x 4096 16.4 and 13.5 us).
+int pick_pair(const Mm &p) {
+  if (tile_count(p, 2 * BR, 64) < 60) return 0;
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (int nt : {256, 192, 128, 64}) {
+    const int64_t cost = (tile_count(p, 2 * BR, nt) + 73) / 74 * (2 * BR + nt);
+    if (cost < least) {
+      least = cost;
+      best = nt;
+    }
+  }
+  return best;
+}
+
+// Few tiles: columns of a tile, and CTAs that share its K.  With a short K as
+// many CTAs as there are to go round, none split (333 x 777 x 1120: 7.2 us in 16
+// columns, 9.8 us in 64).  With a long one at most one tile to two SMs, each
+// split as far as two CTAs an SM and two stages a CTA allow (64 x 4096 x 4096: 11.4 us
+// in 32 columns over 4 CTAs, 15 us in 16 over 2).
+void pick_tile(const Mm &p, int *nt, int *split) {
+  const int chunks = (p.K + BK - 1) / BK;
+  const bool whole = chunks < 16;
+  *nt = 16;
+  while (*nt < 128 && tile_count(p, BR, *nt) > (whole ? 296 : 74)) *nt *= 2;
+  const int64_t tiles = tile_count(p, BR, *nt);
+  *split = 1;
+  while (!whole && *split < MAX_SPLIT && 2 * *split * tiles <= 296 && chunks >= 4 * *split) *split *= 2;
+}
+
 template <typename T, bool TMA>
 bv_status run_typed(const Mm &p, cudaStream_t st) {
-#ifdef BV_INT8_SWEEP
+  // (four columns: 4096 x 4096 9.2 us by dot products, 9.4 us in tiles; eight 11.2 us)
+  if (p.cols <= 4) return run_dots<T>(p, TMA, st);
   if constexpr (TMA) {
-    if (sweep_nt == 256 && sweep_pair) return run_pair<T, 256>(p, st);
-    if (sweep_nt == 128 && sweep_pair) return run_pair<T, 128>(p, st);
+    const int nt = pick_pair(p);
+    if (nt == 256) return run_pair<T, 256>(p, st);
+    if (nt == 192) return run_pair<T, 192>(p, st);
+    if (nt == 128) return run_pair<T, 128>(p, st);
+    if (nt == 64) return run_pair<T, 64>(p, st);
   }
-  if (sweep_nt == 16) return run_tile<T, 16, TMA>(p, st);
-  if (sweep_nt == 32) return run_tile<T, 32, TMA>(p, st);
-  if (sweep_nt == 64) return run_tile<T, 64, TMA>(p, st);
-  return run_tile<T, 128, TMA>(p, st);
-#endif
-  if constexpr (TMA) {
-    if (p.cols > 128 && (int64_t)p.rows * p.cols > (int64_t)1 << 21) return run_pair<T, 256>(p, st);
-  }
-  if (p.cols <= 16) return run_tile<T, 16, TMA>(p, st);
-  if (p.cols <= 32) return run_tile<T, 32, TMA>(p, st);
-  if (p.cols <= 64) return run_tile<T, 64, TMA>(p, st);
-  return run_tile<T, 128, TMA>(p, st);
+  int nt, split;
+  pick_tile(p, &nt, &split);
+  if (nt == 16) return run_tile<T, 16, TMA>(p, split, st);
+  if (nt == 32) return run_tile<T, 32, TMA>(p, split, st);
+  if (nt == 64) return run_tile<T, 64, TMA>(p, split, st);
+  return run_tile<T, 128, TMA>(p, split, st);
 }
 
 }  // namespace

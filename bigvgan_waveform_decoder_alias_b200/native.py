@@ -717,15 +717,22 @@ class BweTail:
 
 
 # --------------------------------------------------------- token operators
+#
+# These are called once a layer and token, where the host's time counts: the
+# common case (contiguous tensors on the current device, its current stream)
+# takes the short way through each check.
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _rows(t: torch.Tensor, name: str):
     """(pointer, stride, rows, cols) of t seen as [rows, cols]: consecutive
     elements within a row, one stride between rows."""
-    if not t.is_cuda:
-        raise BVError(1, f"{name} must be a CUDA tensor")
+    if t.is_contiguous() and t.dim() > 0:
+        cols = t.shape[-1]
+        return t.data_ptr(), cols, (t.numel() // cols if cols else math.prod(t.shape[:-1])), cols
     if t.dim() != 2:
         if t.dim() == 0:
             raise BVError(2, f"{name} needs a last dimension")
@@ -740,50 +747,60 @@ def _rows(t: torch.Tensor, name: str):
     return t.data_ptr(), (stride if rows > 1 else cols), rows, cols
 
 
-def _vec(t: Optional[torch.Tensor], n: int, name: str, dtype=torch.float32):
-    if t is None:
-        return None
-    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise BVError(1, f"{name} must be a contiguous {dtype} CUDA tensor of {n} values")
+def _vec(t: torch.Tensor, n: int, name: str, dtype=torch.float32):
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise BVError(1, f"{name} must be a contiguous {dtype} tensor of {n} values")
     return t.data_ptr()
 
 
 class _On:
-    """The device and stream of a call: the tensors' device is made current,
+    """Another device or stream for a call: the tensors' device is made current,
     and new outputs belong to the stream that writes them."""
 
-    def __init__(self, stream, *tensors):
-        dev = tensors[0].device
-        if dev.type != "cuda":
+    def __init__(self, stream, t):
+        if not t.is_cuda:
             raise BVError(1, "tensors must be CUDA tensors")
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise BVError(1, f"tensors on {dev} and {t.device}")
         self.ctx = []
-        if dev.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(dev))
+        if t.device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(t.device))
         if stream is not None:
-            if stream.device != dev:
-                raise BVError(1, f"tensors on {dev}, the stream on {stream.device}")
+            if stream.device != t.device:
+                raise BVError(1, f"tensors on {t.device}, the stream on {stream.device}")
             self.ctx.append(torch.cuda.stream(stream))
-        self.index = dev.index
 
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
             c.__exit__(*exc)
 
 
-def _int8_rows(shape, device) -> torch.Tensor:
-    """int8 [..., cols] whose rows start on 16 bytes, as bv_int8_matmul reads
-    them fastest: cols of each padded row (the padding holds nothing)."""
-    cols = shape[-1]
-    return torch.empty((*shape[:-1], (cols + 15) // 16 * 16), device=device,
-                       dtype=torch.int8)[..., :cols]
+def _here(stream, t) -> bool:
+    """Does a call on tensor t run on the current device and stream as it is?"""
+    return stream is None and t.is_cuda and t.get_device() == _current_device()
+
+
+def _one_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise BVError(1, f"tensors on cuda:{dev} and {t.device}")
+
+
+def _int8_rows(x) -> torch.Tensor:
+    """int8 [..., cols] of x's shape whose rows start on 16 bytes, as
+    bv_int8_matmul reads them fastest: where cols is no multiple of 16, the
+    cols of each padded row (the padding holds nothing)."""
+    cols = x.shape[-1]
+    if cols % 16 == 0:
+        return torch.empty_like(x, dtype=torch.int8) if x.is_contiguous() else \
+            x.new_empty(x.shape, dtype=torch.int8)
+    return x.new_empty((*x.shape[:-1], (cols + 15) // 16 * 16), dtype=torch.int8)[..., :cols]
+
+
+def _new_like(x) -> torch.Tensor:
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def _like(t, x, dtype, name):
@@ -792,67 +809,104 @@ def _like(t, x, dtype, name):
     return t
 
 
-def _norm_args(x, gain, residual, h):
-    if x.dtype not in DTYPES:
+def _dtype(dtype, name) -> int:
+    dt = DTYPES.get(dtype)
+    if dt is None:
+        raise BVError(1, f"{name} of type {dtype}")
+    return dt
+
+
+def _norm_args(x, gain, residual, h, dev):
+    """The leading arguments of both norms (rows, cols last but one)."""
+    dt = DTYPES.get(x.dtype)
+    if dt is None:
         raise BVError(1, f"x of type {x.dtype}")
     xp, xs, rows, cols = _rows(x, "x")
     rp = hp = gp = None
-    rs = hs = 0
+    rs = hs = gdt = 0
     if residual is not None:
+        if residual.get_device() != dev:
+            _one_device(dev, residual)
         rp, rs, _, _ = _rows(_like(residual, x, x.dtype, "residual"), "residual")
     if h is not None:
+        if h.get_device() != dev:
+            _one_device(dev, h)
         hp, hs, _, _ = _rows(_like(h, x, x.dtype, "h"), "h")
-    gdt = 0
     if gain is not None:
-        if gain.dtype not in DTYPES:
-            raise BVError(1, f"gain of type {gain.dtype}")
-        gdt = DTYPES[gain.dtype]
-        gp = _vec(gain, cols, "gain", gain.dtype)
-    return xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, DTYPES[x.dtype]
+        gdt = DTYPES.get(gain.dtype)
+        if gdt is None or gain.numel() != cols or not gain.is_contiguous() or \
+                gain.get_device() != dev:
+            raise BVError(1, f"gain must be {cols} contiguous values of x's type or f32 on x's device")
+        gp = gain.data_ptr()
+    return xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt
 
 
 def bv_rms_norm(x, gain=None, eps=1e-6, residual=None, h=None, y=None, stream=None):
     """Root-mean-square norm of the rows of x [..., cols] (+ residual) times
     gain [cols].  Returns y, with a residual (y, h), h = x + residual in x's
     type; h may be given, and may be x or the residual itself."""
-    with _On(stream, x, gain, residual, h, y) as st:
-        if residual is not None and h is None:
-            h = torch.empty_like(x, memory_format=torch.contiguous_format)
-        xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h)
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else y
+    if not _here(stream, x):
+        with _On(stream, x):
+            return bv_rms_norm(x, gain, eps, residual, h, y)
+    if residual is not None and h is None:
+        h = _new_like(x)
+    dev = x.get_device()
+    xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h, dev)
+    if y is None:
+        y = _new_like(x)
+        yp, ys = y.data_ptr(), cols
+    else:
+        _one_device(dev, y)
         yp, ys, _, _ = _rows(_like(y, x, x.dtype, "y"), "y")
-        _check(lib().bv_rms_norm(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, yp, ys, st))
+    _check(lib().bv_rms_norm(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, yp, ys,
+                             _raw_stream(dev)))
     return y if residual is None else (y, h)
+
+
+def _int8_out(x, q, scale, rows, dev):
+    """q and scale of x's rows (new ones where None), q's pointer and stride."""
+    if q is None:
+        q = _int8_rows(x)
+    else:
+        _one_device(dev, _like(q, x, torch.int8, "q"))
+    if scale is None:
+        scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
+        sp = scale.data_ptr()
+    else:
+        _one_device(dev, scale)
+        sp = _vec(scale, rows, "scale")
+    qp, qs, _, _ = _rows(q, "q")
+    return q, scale, qp, qs, sp
 
 
 def bv_rms_norm_int8(x, gain=None, eps=1e-6, residual=None, h=None, q=None, scale=None,
                      stream=None):
     """bv_rms_norm with 8-bit rows: (q int8 [..., cols], scale f32 [...]) with
     y = q scale, and h as a third with a residual."""
-    with _On(stream, x, gain, residual, h, q, scale) as st:
-        if residual is not None and h is None:
-            h = torch.empty_like(x, memory_format=torch.contiguous_format)
-        xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h)
-        q = _int8_rows(x.shape, x.device) if q is None else q
-        qp, qs, _, _ = _rows(_like(q, x, torch.int8, "q"), "q")
-        scale = torch.empty(x.shape[:-1], device=x.device) if scale is None else scale
-        _check(lib().bv_rms_norm_int8(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, qp, qs,
-                                      _vec(scale, rows, "scale"), st))
+    if not _here(stream, x):
+        with _On(stream, x):
+            return bv_rms_norm_int8(x, gain, eps, residual, h, q, scale)
+    if residual is not None and h is None:
+        h = _new_like(x)
+    dev = x.get_device()
+    xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h, dev)
+    q, scale, qp, qs, sp = _int8_out(x, q, scale, rows, dev)
+    _check(lib().bv_rms_norm_int8(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, qp, qs, sp,
+                                  _raw_stream(dev)))
     return (q, scale) if residual is None else (q, scale, h)
 
 
 def bv_quantize_rows(x, q=None, scale=None, stream=None):
     """The rows of x [..., cols] in 8 bits: (q int8 [..., cols], scale f32
     [...]); tokens [M, K] or a weight [N, K] for bv_int8_matmul."""
-    if x.dtype not in DTYPES:
-        raise BVError(1, f"x of type {x.dtype}")
-    with _On(stream, x, q, scale) as st:
-        xp, xs, rows, cols = _rows(x, "x")
-        q = _int8_rows(x.shape, x.device) if q is None else q
-        qp, qs, _, _ = _rows(_like(q, x, torch.int8, "q"), "q")
-        scale = torch.empty(x.shape[:-1], device=x.device) if scale is None else scale
-        _check(lib().bv_quantize_rows(xp, xs, rows, cols, DTYPES[x.dtype], qp, qs,
-                                      _vec(scale, rows, "scale"), st))
+    if not _here(stream, x):
+        with _On(stream, x):
+            return bv_quantize_rows(x, q, scale)
+    dt = _dtype(x.dtype, "x")
+    dev = x.get_device()
+    xp, xs, rows, cols = _rows(x, "x")
+    q, scale, qp, qs, sp = _int8_out(x, q, scale, rows, dev)
+    _check(lib().bv_quantize_rows(xp, xs, rows, cols, dt, qp, qs, sp, _raw_stream(dev)))
     return q, scale
 
 
@@ -861,30 +915,42 @@ def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=N
     """a int8 [..., K] (scales a_scale [...]) times w int8 [N, K] (w_scale
     [N]): y [..., N], or with channels_first [N, tokens].  out_dtype: f32 (the
     default), bf16 or f16; y's or the residual's where one is given."""
+    if not _here(stream, a):
+        with _On(stream, a):
+            return bv_int8_matmul(a, a_scale, w, w_scale, bias, residual, out_dtype,
+                                  channels_first, y)
     if a.dtype != torch.int8 or w.dtype != torch.int8:
         raise BVError(1, "a and w must be int8")
-    with _On(stream, a, a_scale, w, w_scale, bias, residual, y) as st:
-        ap, as_, M, K = _rows(a, "a")
-        wp, ws, N, Kw = _rows(w, "w")
-        if w.dim() != 2 or K != Kw:
-            raise BVError(2, f"a [..., {K}] times w {tuple(w.shape)}")
-        if out_dtype is None:
-            out_dtype = (y if y is not None else residual).dtype \
-                if y is not None or residual is not None else torch.float32
-        if out_dtype not in DTYPES:
-            raise BVError(1, f"y of type {out_dtype}")
-        shape = (N, M) if channels_first else (*a.shape[:-1], N)
-        y = torch.empty(shape, device=a.device, dtype=out_dtype) if y is None else y
-        if tuple(y.shape) != shape or y.dtype != out_dtype:
-            raise BVError(2, f"y must be {out_dtype} of shape {shape}")
+    ap, as_, M, K = _rows(a, "a")
+    wp, ws, N, Kw = _rows(w, "w")
+    if w.dim() != 2 or K != Kw:
+        raise BVError(2, f"a [..., {K}] times w {tuple(w.shape)}")
+    if out_dtype is None:
+        out_dtype = y.dtype if y is not None else \
+            residual.dtype if residual is not None else torch.float32
+    dt = _dtype(out_dtype, "y")
+    dev = a.get_device()
+    shape = (N, M) if channels_first else (M, N) if a.dim() == 2 else (*a.shape[:-1], N)
+    if y is None:
+        y = a.new_empty(shape, dtype=out_dtype)
+        yp, ys = y.data_ptr(), shape[-1]
+    else:
+        if y.shape != shape or y.dtype != out_dtype:
+            raise BVError(2, f"y must be {out_dtype} of shape {tuple(shape)}")
+        _one_device(dev, y)
         yp, ys, _, _ = _rows(y, "y")
-        rp, rs = None, 0
-        if residual is not None:
-            rp, rs, _, _ = _rows(_like(residual, y, out_dtype, "residual"), "residual")
-        _check(lib().bv_int8_matmul(ap, as_, _vec(a_scale, M, "a_scale"), wp, ws,
-                                    _vec(w_scale, N, "w_scale"), _vec(bias, N, "bias"), M, N, K,
-                                    rp, rs, yp, ys, DTYPES[out_dtype], int(bool(channels_first)),
-                                    st))
+    rp, rs, bp = None, 0, None
+    if residual is not None:
+        _one_device(dev, residual)
+        rp, rs, _, _ = _rows(_like(residual, y, out_dtype, "residual"), "residual")
+    if bias is not None:
+        _one_device(dev, bias)
+        bp = _vec(bias, N, "bias")
+    if w.get_device() != dev or a_scale.get_device() != dev or w_scale.get_device() != dev:
+        _one_device(dev, w, a_scale, w_scale)
+    _check(lib().bv_int8_matmul(ap, as_, _vec(a_scale, M, "a_scale"), wp, ws,
+                                _vec(w_scale, N, "w_scale"), bp, M, N, K, rp, rs, yp, ys, dt,
+                                1 if channels_first else 0, _raw_stream(dev)))
     return y
 
 
@@ -912,22 +978,28 @@ class TokenFrontEnd:
         Cout = self.w.shape[0]
         if D != self.w.shape[1]:
             raise BVError(2, f"x [..., {D}], weight {tuple(self.w.shape)}")
-        with _On(stream, x, residual, self.gain, self.w, self.bias, z, workspace) as st:
-            xp, xs, rp, rs, _, _, gp, gdt, rows, cols, dt = _norm_args(x, self.gain, residual, None)
-            shape = (S, Cout, T) if by_side else (Cout, S, T)
-            if z is None:
-                z = torch.empty(shape, device=x.device, dtype=torch.float32)
-            elif tuple(z.shape) != shape:
-                raise BVError(2, f"z must have shape {shape}")
-            need = int(lib().bv_token_front_end_workspace_size(S, T, D))
-            if need == 0:
-                raise BVError(2, last_error())
-            if workspace is None:
-                workspace = torch.empty(need // 4 + 64, device=x.device, dtype=torch.float32)
-            _check(lib().bv_token_front_end(xp, xs, rp, rs, gp, gdt, self.eps, S, T, D, dt,
-                                            self.w.data_ptr(), self.w.stride(0),
-                                            _vec(self.w_scale, Cout, "w_scale"),
-                                            _vec(self.bias, Cout, "bias"), Cout,
-                                            int(bool(by_side)), _ptr(z), _ptr(workspace),
-                                            workspace.numel() * 4, st))
+        if not _here(stream, x):
+            with _On(stream, x):
+                return self(x, residual, by_side, z, workspace)
+        shape = (S, Cout, T) if by_side else (Cout, S, T)
+        if z is None:
+            z = x.new_empty(shape, dtype=torch.float32)
+        elif tuple(z.shape) != shape:
+            raise BVError(2, f"z must have shape {shape}")
+        need = int(lib().bv_token_front_end_workspace_size(S, T, D))
+        if need == 0:
+            raise BVError(2, last_error())
+        if workspace is None:
+            workspace = x.new_empty(need // 4 + 64, dtype=torch.float32)
+        dev = x.get_device()
+        _one_device(dev, self.w, self.bias, z, workspace)
+        xp, xs, rp, rs, _, _, gp, gdt, rows, cols, dt = _norm_args(x, self.gain, residual, None,
+                                                                     dev)
+        _check(lib().bv_token_front_end(xp, xs, rp, rs, gp, gdt, self.eps, S, T, D, dt,
+                                        self.w.data_ptr(), self.w.stride(0),
+                                        self.w_scale.data_ptr(),
+                                        None if self.bias is None else
+                                        _vec(self.bias, Cout, "bias"), Cout,
+                                        int(bool(by_side)), _ptr(z), _ptr(workspace),
+                                        workspace.numel() * 4, _raw_stream(dev)))
         return z
