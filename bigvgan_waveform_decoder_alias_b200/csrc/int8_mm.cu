@@ -158,39 +158,56 @@ __host__ __device__ constexpr int tmem_cols(int n) {
   return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512;
 }
 
-// 16 bytes of K from byte k on of a row, zero past K.  Aligned words are
-// read where the whole word lies inside the operand [lo, hi), else bytes.
-__device__ __forceinline__ uint4 load16(const int8_t *row, int k, int K, const int8_t *lo,
+// 16 bytes of K from byte k on of a row that starts anywhere, zero past K: the
+// one or two aligned 16-byte words that hold them are read (fetch), then
+// shifted into place (bytes).  Near the ends of the operand [lo, hi), where a
+// word would reach outside, single bytes are read.
+struct Piece {
+  uint4 a, b;
+  int off, n;  // where the bytes begin in a; how many are inside K
+
+  __device__ __forceinline__ void fetch(const int8_t *row, int k, int K, const int8_t *lo,
                                         const int8_t *hi) {
-  uint4 out = make_uint4(0, 0, 0, 0);
-  const int nb = min(16, K - k);
-  if (nb <= 0) return out;
-  const int8_t *p = row + k;
-  const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3);
-  const int8_t *a = p - sh;
-  unsigned w[5];
+    a = b = make_uint4(0, 0, 0, 0);
+    off = 0;
+    n = min(16, K - k);
+    if (n <= 0) return;
+    const int8_t *p = row + k;
+    const int at = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    const int8_t *w = p - at;
+    const bool two = at + n > 16;
+    if (w >= lo && w + (two ? 32 : 16) <= hi) {
+      off = at;
+      a = __ldg(reinterpret_cast<const uint4 *>(w));
+      if (two) b = __ldg(reinterpret_cast<const uint4 *>(w) + 1);
+    } else {
+      unsigned v[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 5; ++i) {
-    w[i] = 0;
-    const int8_t *q = a + 4 * i;
-    if (q < p + nb) {
-      if (q >= lo && q + 4 <= hi) {
-        w[i] = __ldg(reinterpret_cast<const unsigned *>(q));
-      } else {
-        for (int b = 0; b < 4; ++b)
-          if (q + b >= lo && q + b < hi) w[i] |= (unsigned)(uint8_t)__ldg(q + b) << (8 * b);
-      }
+      for (int i = 0; i < 16; ++i)
+        if (i < n) v[i / 4] |= (unsigned)(uint8_t)__ldg(p + i) << (8 * (i % 4));
+      a = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
-  unsigned v[4];
+  __device__ __forceinline__ uint4 bytes() const {
+    unsigned w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = __funnelshift_r(w[i], w[i + 1], 8 * sh);
-    const int left = nb - 4 * i;  // bytes of this word inside K
-    if (left < 4) v[i] = left <= 0 ? 0u : v[i] & (0xffffffffu >> (32 - 8 * left));
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    unsigned v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __funnelshift_r(w[i], w[i + 1], 8 * (off & 3));
+      const int left = n - 4 * i;  // bytes of this word inside K
+      if (left < 4) v[i] = left <= 0 ? 0u : v[i] & (0xffffffffu >> (32 - 8 * left));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
   }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
+};
 
 // ------------------------------------------------------------- few columns
 //
@@ -201,8 +218,8 @@ __device__ __forceinline__ uint4 load16(const int8_t *row, int k, int K, const i
 
 constexpr int DOT_THREADS = 128;
 
-template <typename T, int R, int C>
-__global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p, bool aligned) {
+template <typename T, int R, int C, bool ALIGNED>
+__global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p) {
   __shared__ int part[DOT_THREADS / 32][R * C];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = (int)blockIdx.x * R;
@@ -211,16 +228,27 @@ __global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p, bool 
   int acc[R][C] = {};
   for (int k = 16 * threadIdx.x; k < p.K; k += 16 * DOT_THREADS) {
     uint4 r[R], c[C];
-    const bool whole = aligned && k + 16 <= p.K;
+    if (ALIGNED && k + 16 <= p.K) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int8_t *row = p.r + (int64_t)min(row0 + i, p.rows - 1) * p.rstride;
-      r[i] = whole ? __ldg(reinterpret_cast<const uint4 *>(row + k)) : load16(row, k, p.K, p.r, rhi);
-    }
+      for (int i = 0; i < R; ++i)
+        r[i] = __ldg(reinterpret_cast<const uint4 *>(
+            p.r + (int64_t)min(row0 + i, p.rows - 1) * p.rstride + k));
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int8_t *col = p.c + (int64_t)min(j, p.cols - 1) * p.cstride;
-      c[j] = whole ? __ldg(reinterpret_cast<const uint4 *>(col + k)) : load16(col, k, p.K, p.c, chi);
+      for (int j = 0; j < C; ++j)
+        c[j] = __ldg(reinterpret_cast<const uint4 *>(
+            p.c + (int64_t)min(j, p.cols - 1) * p.cstride + k));
+    } else {
+      Piece pr[R], pc[C];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        pr[i].fetch(p.r + (int64_t)min(row0 + i, p.rows - 1) * p.rstride, k, p.K, p.r, rhi);
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        pc[j].fetch(p.c + (int64_t)min(j, p.cols - 1) * p.cstride, k, p.K, p.c, chi);
+#pragma unroll
+      for (int i = 0; i < R; ++i) r[i] = pr[i].bytes();
+#pragma unroll
+      for (int j = 0; j < C; ++j) c[j] = pc[j].bytes();
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -270,8 +298,9 @@ __global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p, bool 
 // the join's order does not show.  (Adding to the owner's shared memory from
 // afar instead took longer: 16 x 8192 x 2048 11.2 us, 10.0 us so.)
 //
-// TMA: thread 0 loads the stages by TMA.  Otherwise (rows that do not start on
-// 16 bytes) warps 4..7 copy them: aligned words, shifted into place.
+// Thread 0 loads the stages by TMA.  Where an operand's rows do not start on 16
+// bytes (COPY_R, COPY_C) eight more warps copy that operand instead: aligned
+// words, shifted into place, all of a stage's reads issued before its writes.
 
 constexpr int TILE_MAX_STAGES = 12;
 
@@ -280,12 +309,15 @@ constexpr int tile_stage_bytes() {
   return (BR + NT) * BK;
 }
 
-template <typename T, int NT, bool TMA>
-__global__ void __launch_bounds__(TMA ? 128 : 256)
+constexpr int COPY_WARPS = 8;
+
+template <typename T, int NT, bool COPY_R, bool COPY_C>
+__global__ void __launch_bounds__(COPY_R || COPY_C ? 128 + 32 * COPY_WARPS : 128)
 int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_c,
                  const Mm p, int tiles_r, int split, int stages, int *status,
                  long long wait_limit) {
   constexpr int STAGE = tile_stage_bytes<NT>();
+  constexpr bool COPY = COPY_R || COPY_C, TMA = !COPY_R || !COPY_C;
   constexpr unsigned TMEM = tmem_cols(NT);
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -305,13 +337,11 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   const WaitCtx wc{&ctl, 0u, status, wait_limit};
 
   if (threadIdx.x == 0) {
-    if (TMA) {
-      prefetch_map(&map_r);
-      prefetch_map(&map_c);
-    }
+    if (!COPY_R) prefetch_map(&map_r);
+    if (!COPY_C) prefetch_map(&map_c);
     ctl.abort = 0;
     for (int s = 0; s < stages; ++s) {
-      mbar_init(bar_full + 8 * s, TMA ? 1 : 4);
+      mbar_init(bar_full + 8 * s, (TMA ? 1 : 0) + (COPY ? COPY_WARPS : 0));
       mbar_init(bar_empty + 8 * s, 1);
     }
     mbar_init(bar_done, 1);
@@ -346,9 +376,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
       const int s = c % stages, u = c / stages;
       if (u > 0 && !mbar_wait(bar_empty + 8 * s, (u - 1) & 1, wc, 301)) break;
       const unsigned dst = smem_u32(smem + s * STAGE), fb = bar_full + 8 * s;
-      mbar_arrive_tx(fb, STAGE);
-      tma_load_2d(dst, &map_r, (c0 + c) * BK, row0, fb);
-      tma_load_2d(dst + BR * BK, &map_c, (c0 + c) * BK, col0, fb);
+      mbar_arrive_tx(fb, (COPY_R ? 0 : BR * BK) + (COPY_C ? 0 : NT * BK));
+      if (!COPY_R) tma_load_2d(dst, &map_r, (c0 + c) * BK, row0, fb);
+      if (!COPY_C) tma_load_2d(dst + BR * BK, &map_c, (c0 + c) * BK, col0, fb);
     }
     // the last load into each slot has landed before the CTA can exit
     for (int d = c - stages; d < c; ++d)
@@ -367,35 +397,39 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
     }
     mma_commit(bar_done);
     mbar_drain(bar_done, 0);  // after an abort too, no MMA outlives the tile
-  } else if (!TMA && warp >= 4) {
-    // each warp's lanes take 4 rows x 8 pieces of 16 bytes at a time
-    const int8_t *rlo = p.r, *rhi = p.r + (int64_t)(p.rows - 1) * p.rstride + p.K;
-    const int8_t *clo = p.c, *chi = p.c + (int64_t)(p.cols - 1) * p.cstride + p.K;
-    const int piece = lane & 7, sub = (warp - 4) * 4 + (lane >> 3);  // 16 rows a pass
+  } else if (COPY && warp >= 4) {
+    // a warp's lanes take 4 rows x 8 pieces of 16 bytes at a time
+    const int8_t *rhi = p.r + (int64_t)(p.rows - 1) * p.rstride + p.K;
+    const int8_t *chi = p.c + (int64_t)(p.cols - 1) * p.cstride + p.K;
+    const int piece = lane & 7, sub = (warp - 4) * 4 + (lane >> 3);
+    constexpr int PASS = 4 * COPY_WARPS;  // rows a pass over the warps
+    // rows [first, last) of a stage: BR rows, then NT columns
+    constexpr int FIRST = COPY_R ? 0 : BR, LAST = COPY_C ? BR + NT : BR;
     for (int c = 0; c < n; ++c) {
       const int s = c % stages, u = c / stages;
       if (u > 0 && !warp_wait(bar_empty + 8 * s, (u - 1) & 1, wc, 303)) break;
       unsigned char *at = smem + s * STAGE;
       const int k = (c0 + c) * BK + 16 * piece;
 #pragma unroll
-      for (int g = 0; g < (BR + NT) / 16; g += 4) {
-        uint4 v[4];
+      for (int g = FIRST; g < LAST; g += 4 * PASS) {
+        Piece v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = 16 * (g + i) + sub;  // row of the stage: BR rows, then NT columns
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (16 * (g + i) >= BR + NT) continue;
+          const int r = g + i * PASS + sub;
+          if (g + i * PASS >= LAST) continue;
           if (r < BR) {
-            if (row0 + r < p.rows) v[i] = load16(p.r + (row0 + r) * p.rstride, k, p.K, rlo, rhi);
-          } else if (col0 + r - BR < p.cols) {
-            v[i] = load16(p.c + (col0 + r - BR) * p.cstride, k, p.K, clo, chi);
+            const bool have = row0 + r < p.rows;
+            v[i].fetch(p.r + (have ? row0 + r : 0) * p.rstride, k, have ? p.K : 0, p.r, rhi);
+          } else {
+            const bool have = r < LAST && col0 + r - BR < p.cols;
+            v[i].fetch(p.c + (have ? col0 + r - BR : 0) * p.cstride, k, have ? p.K : 0, p.c, chi);
           }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = 16 * (g + i) + sub;
-          if (16 * (g + i) < BR + NT)
-            *reinterpret_cast<uint4 *>(at + r * BK + ((piece ^ (r & 7)) << 4)) = v[i];
+          const int r = g + i * PASS + sub;
+          if (g + i * PASS < LAST && r < LAST)
+            *reinterpret_cast<uint4 *>(at + r * BK + ((piece ^ (r & 7)) << 4)) = v[i].bytes();
         }
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -720,7 +754,7 @@ bv_status encode_rows(CUtensorMap *map, const int8_t *p, int64_t stride, int row
   return BV_OK;
 }
 
-template <typename T, int NT, bool TMA>
+template <typename T, int NT, bool COPY_R, bool COPY_C>
 bv_status run_tile(const Mm &p, int split, cudaStream_t st) {
   const int64_t tiles_r = ((int64_t)p.rows + BR - 1) / BR, tiles_c = ((int64_t)p.cols + NT - 1) / NT;
   const int64_t tiles = tiles_r * tiles_c;
@@ -733,19 +767,17 @@ bv_status run_tile(const Mm &p, int split, cudaStream_t st) {
   const int least = split > 1 ? (NT * BR * 4 + STAGE - 1) / STAGE : 1;
   stages = std::max(stages, least);
   const size_t smem = (size_t)stages * STAGE + 1024;
-  auto kernel = int8_tile_kernel<T, NT, TMA>;
+  auto kernel = int8_tile_kernel<T, NT, COPY_R, COPY_C>;
   // (room beside the kernel's static shared memory too)
   BV_TRY(ensure_dynamic_smem((const void *)kernel, smem + 2048, "bv_int8_matmul smem"));
   CUtensorMap mr{}, mc{};
-  if (TMA) {
-    BV_TRY(encode_rows(&mr, p.r, p.rstride, p.rows, p.K, BR));
-    BV_TRY(encode_rows(&mc, p.c, p.cstride, p.cols, p.K, NT));
-  }
+  if (!COPY_R) BV_TRY(encode_rows(&mr, p.r, p.rstride, p.rows, p.K, BR));
+  if (!COPY_C) BV_TRY(encode_rows(&mc, p.c, p.cstride, p.cols, p.K, NT));
   int *status = device_status_ptr();
   if (!status) return fail(BV_ERR_CUDA, "bv_int8_matmul: status word");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split));
-  cfg.blockDim = dim3(TMA ? 128 : 256);
+  cfg.blockDim = dim3(COPY_R || COPY_C ? 128 + 32 * COPY_WARPS : 128);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -779,25 +811,26 @@ bv_status run_pair(const Mm &p, cudaStream_t st) {
   return BV_OK;
 }
 
-template <typename T, int R, int C>
-bv_status run_dot(const Mm &p, bool aligned, cudaStream_t st) {
-  int8_dot_kernel<T, R, C><<<(unsigned)((p.rows + (int64_t)R - 1) / R), DOT_THREADS, 0, st>>>(p, aligned);
+template <typename T, int R, int C, bool ALIGNED>
+bv_status run_dot(const Mm &p, cudaStream_t st) {
+  int8_dot_kernel<T, R, C, ALIGNED>
+      <<<(unsigned)((p.rows + (int64_t)R - 1) / R), DOT_THREADS, 0, st>>>(p);
   return BV_OK;
 }
-template <typename T, int C>
-bv_status run_dot_rows(const Mm &p, bool aligned, cudaStream_t st) {
+template <typename T, int C, bool ALIGNED>
+bv_status run_dot_rows(const Mm &p, cudaStream_t st) {
   // the most rows a block that leave three blocks an SM
   const int blocks = 3 * 148;
-  if (p.rows >= 8 * blocks) return run_dot<T, 8, C>(p, aligned, st);
-  if (p.rows >= 4 * blocks) return run_dot<T, 4, C>(p, aligned, st);
-  if (p.rows >= 2 * blocks) return run_dot<T, 2, C>(p, aligned, st);
-  return run_dot<T, 1, C>(p, aligned, st);
+  if (p.rows >= 8 * blocks) return run_dot<T, 8, C, ALIGNED>(p, st);
+  if (p.rows >= 4 * blocks) return run_dot<T, 4, C, ALIGNED>(p, st);
+  if (p.rows >= 2 * blocks) return run_dot<T, 2, C, ALIGNED>(p, st);
+  return run_dot<T, 1, C, ALIGNED>(p, st);
 }
-template <typename T>
-bv_status run_dots(const Mm &p, bool aligned, cudaStream_t st) {
-  if (p.cols == 1) return run_dot_rows<T, 1>(p, aligned, st);
-  if (p.cols == 2) return run_dot_rows<T, 2>(p, aligned, st);
-  return run_dot_rows<T, 4>(p, aligned, st);
+template <typename T, bool ALIGNED>
+bv_status run_dots(const Mm &p, cudaStream_t st) {
+  if (p.cols == 1) return run_dot_rows<T, 1, ALIGNED>(p, st);
+  if (p.cols == 2) return run_dot_rows<T, 2, ALIGNED>(p, st);
+  return run_dot_rows<T, 4, ALIGNED>(p, st);
 }
 
 int64_t tile_count(const Mm &p, int rows, int cols) {
@@ -838,23 +871,31 @@ void pick_tile(const Mm &p, int *nt, int *split) {
   while (!whole && *split < MAX_SPLIT && 2 * *split * tiles <= 296 && chunks >= 4 * *split) *split *= 2;
 }
 
-template <typename T, bool TMA>
-bv_status run_typed(const Mm &p, cudaStream_t st) {
-  // (four columns: 4096 x 4096 9.2 us by dot products, 9.4 us in tiles; eight 11.2 us)
-  if (p.cols <= 4) return run_dots<T>(p, TMA, st);
-  if constexpr (TMA) {
-    const int nt = pick_pair(p);
-    if (nt == 256) return run_pair<T, 256>(p, st);
-    if (nt == 192) return run_pair<T, 192>(p, st);
-    if (nt == 128) return run_pair<T, 128>(p, st);
-    if (nt == 64) return run_pair<T, 64>(p, st);
-  }
+template <typename T, bool COPY_R, bool COPY_C>
+bv_status run_tiles(const Mm &p, cudaStream_t st) {
   int nt, split;
   pick_tile(p, &nt, &split);
-  if (nt == 16) return run_tile<T, 16, TMA>(p, split, st);
-  if (nt == 32) return run_tile<T, 32, TMA>(p, split, st);
-  if (nt == 64) return run_tile<T, 64, TMA>(p, split, st);
-  return run_tile<T, 128, TMA>(p, split, st);
+  if (nt == 16) return run_tile<T, 16, COPY_R, COPY_C>(p, split, st);
+  if (nt == 32) return run_tile<T, 32, COPY_R, COPY_C>(p, split, st);
+  if (nt == 64) return run_tile<T, 64, COPY_R, COPY_C>(p, split, st);
+  return run_tile<T, 128, COPY_R, COPY_C>(p, split, st);
+}
+
+template <typename T>
+bv_status run_typed(const Mm &p, cudaStream_t st) {
+  const bool tma_r = tma_rows(p.r, p.rstride, p.rows, p.K);
+  const bool tma_c = tma_rows(p.c, p.cstride, p.cols, p.K);
+  // (four columns: 4096 x 4096 9.2 us by dot products, 9.4 us in tiles; eight 11.2 us)
+  if (p.cols <= 4) return tma_r && tma_c ? run_dots<T, true>(p, st) : run_dots<T, false>(p, st);
+  if (!tma_r && !tma_c) return run_tiles<T, true, true>(p, st);
+  if (!tma_r) return run_tiles<T, true, false>(p, st);
+  if (!tma_c) return run_tiles<T, false, true>(p, st);
+  const int nt = pick_pair(p);
+  if (nt == 256) return run_pair<T, 256>(p, st);
+  if (nt == 192) return run_pair<T, 192>(p, st);
+  if (nt == 128) return run_pair<T, 128>(p, st);
+  if (nt == 64) return run_pair<T, 64>(p, st);
+  return run_tiles<T, false, false>(p, st);
 }
 
 }  // namespace
@@ -879,18 +920,13 @@ bv_status launch_int8_matmul(const Int8Args &a, int dtype, cudaStream_t st) {
   p.rs = a.rs;
   p.ys = a.ys;
   p.pairs = aligned_to(a.y, 4) && (a.ys % 2 == 0 || p.cols == 1);
-  const bool tma = tma_rows(p.r, p.rstride, p.rows, p.K) && tma_rows(p.c, p.cstride, p.cols, p.K);
   const double out = (double)a.M * a.N;
   {
     LaunchTimer t(st, "int8_matmul", 2.0 * out * a.K,
                   ((double)a.M + a.N) * a.K + out * dtype_size(dtype) * (a.residual ? 2 : 1));
-    if (dtype == BV_F32)
-      BV_TRY((tma ? run_typed<float, true>(p, st) : run_typed<float, false>(p, st)));
-    else if (dtype == BV_BF16)
-      BV_TRY((tma ? run_typed<__nv_bfloat16, true>(p, st)
-                  : run_typed<__nv_bfloat16, false>(p, st)));
-    else
-      BV_TRY((tma ? run_typed<__half, true>(p, st) : run_typed<__half, false>(p, st)));
+    if (dtype == BV_F32) BV_TRY(run_typed<float>(p, st));
+    else if (dtype == BV_BF16) BV_TRY(run_typed<__nv_bfloat16>(p, st));
+    else BV_TRY(run_typed<__half>(p, st));
   }
   count_launch();
   return check_launch("int8_matmul");

@@ -777,9 +777,10 @@ class _On:
             c.__exit__(*exc)
 
 
-def _here(stream, t) -> bool:
-    """Does a call on tensor t run on the current device and stream as it is?"""
-    return stream is None and t.is_cuda and t.get_device() == _current_device()
+def _here(stream, dev) -> bool:
+    """Does a call on a tensor of device `dev` (-1: host) run on the current device and
+    stream as it is?"""
+    return stream is None and dev >= 0 and dev == _current_device()
 
 
 def _one_device(dev, *tensors):
@@ -818,20 +819,17 @@ def _dtype(dtype, name) -> int:
 
 def _norm_args(x, gain, residual, h, dev):
     """The leading arguments of both norms (rows, cols last but one)."""
-    dt = DTYPES.get(x.dtype)
+    dtype = x.dtype
+    dt = DTYPES.get(dtype)
     if dt is None:
-        raise BVError(1, f"x of type {x.dtype}")
+        raise BVError(1, f"x of type {dtype}")
     xp, xs, rows, cols = _rows(x, "x")
     rp = hp = gp = None
     rs = hs = gdt = 0
     if residual is not None:
-        if residual.get_device() != dev:
-            _one_device(dev, residual)
-        rp, rs, _, _ = _rows(_like(residual, x, x.dtype, "residual"), "residual")
+        rp, rs = _same_rows(residual, x, cols, dev, "residual")
     if h is not None:
-        if h.get_device() != dev:
-            _one_device(dev, h)
-        hp, hs, _, _ = _rows(_like(h, x, x.dtype, "h"), "h")
+        hp, hs = _same_rows(h, x, cols, dev, "h")
     if gain is not None:
         gdt = DTYPES.get(gain.dtype)
         if gdt is None or gain.numel() != cols or not gain.is_contiguous() or \
@@ -841,25 +839,37 @@ def _norm_args(x, gain, residual, h, dev):
     return xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt
 
 
+def _same_rows(t, x, cols, dev, name):
+    """(pointer, stride) of a tensor of x's shape, type and device."""
+    if t.dtype is not x.dtype or t.shape != x.shape:
+        raise BVError(2, f"{name} must be {x.dtype} of shape {tuple(x.shape)}")
+    if t.get_device() != dev:
+        _one_device(dev, t)
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    return _rows(t, name)[:2]
+
+
 def bv_rms_norm(x, gain=None, eps=1e-6, residual=None, h=None, y=None, stream=None):
     """Root-mean-square norm of the rows of x [..., cols] (+ residual) times
     gain [cols].  Returns y, with a residual (y, h), h = x + residual in x's
     type; h may be given, and may be x or the residual itself."""
-    if not _here(stream, x):
+    dev = x.get_device()
+    if not _here(stream, dev):
         with _On(stream, x):
             return bv_rms_norm(x, gain, eps, residual, h, y)
     if residual is not None and h is None:
         h = _new_like(x)
-    dev = x.get_device()
     xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h, dev)
     if y is None:
         y = _new_like(x)
         yp, ys = y.data_ptr(), cols
     else:
-        _one_device(dev, y)
-        yp, ys, _, _ = _rows(_like(y, x, x.dtype, "y"), "y")
-    _check(lib().bv_rms_norm(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, yp, ys,
-                             _raw_stream(dev)))
+        yp, ys = _same_rows(y, x, cols, dev, "y")
+    st = (_LIB or lib()).bv_rms_norm(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, yp, ys,
+                                     _raw_stream(dev))
+    if st:
+        _check(st)
     return y if residual is None else (y, h)
 
 
@@ -867,15 +877,16 @@ def _int8_out(x, q, scale, rows, dev):
     """q and scale of x's rows (new ones where None), q's pointer and stride."""
     if q is None:
         q = _int8_rows(x)
+        qp, qs = q.data_ptr(), (x.shape[-1] + 15) // 16 * 16
     else:
         _one_device(dev, _like(q, x, torch.int8, "q"))
+        qp, qs, _, _ = _rows(q, "q")
     if scale is None:
         scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
         sp = scale.data_ptr()
     else:
         _one_device(dev, scale)
         sp = _vec(scale, rows, "scale")
-    qp, qs, _, _ = _rows(q, "q")
     return q, scale, qp, qs, sp
 
 
@@ -883,27 +894,29 @@ def bv_rms_norm_int8(x, gain=None, eps=1e-6, residual=None, h=None, q=None, scal
                      stream=None):
     """bv_rms_norm with 8-bit rows: (q int8 [..., cols], scale f32 [...]) with
     y = q scale, and h as a third with a residual."""
-    if not _here(stream, x):
+    dev = x.get_device()
+    if not _here(stream, dev):
         with _On(stream, x):
             return bv_rms_norm_int8(x, gain, eps, residual, h, q, scale)
     if residual is not None and h is None:
         h = _new_like(x)
-    dev = x.get_device()
     xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h, dev)
     q, scale, qp, qs, sp = _int8_out(x, q, scale, rows, dev)
-    _check(lib().bv_rms_norm_int8(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, qp, qs, sp,
-                                  _raw_stream(dev)))
+    st = (_LIB or lib()).bv_rms_norm_int8(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, qp,
+                                          qs, sp, _raw_stream(dev))
+    if st:
+        _check(st)
     return (q, scale) if residual is None else (q, scale, h)
 
 
 def bv_quantize_rows(x, q=None, scale=None, stream=None):
     """The rows of x [..., cols] in 8 bits: (q int8 [..., cols], scale f32
     [...]); tokens [M, K] or a weight [N, K] for bv_int8_matmul."""
-    if not _here(stream, x):
+    dev = x.get_device()
+    if not _here(stream, dev):
         with _On(stream, x):
             return bv_quantize_rows(x, q, scale)
     dt = _dtype(x.dtype, "x")
-    dev = x.get_device()
     xp, xs, rows, cols = _rows(x, "x")
     q, scale, qp, qs, sp = _int8_out(x, q, scale, rows, dev)
     _check(lib().bv_quantize_rows(xp, xs, rows, cols, dt, qp, qs, sp, _raw_stream(dev)))
@@ -915,7 +928,8 @@ def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=N
     """a int8 [..., K] (scales a_scale [...]) times w int8 [N, K] (w_scale
     [N]): y [..., N], or with channels_first [N, tokens].  out_dtype: f32 (the
     default), bf16 or f16; y's or the residual's where one is given."""
-    if not _here(stream, a):
+    dev = a.get_device()
+    if not _here(stream, dev):
         with _On(stream, a):
             return bv_int8_matmul(a, a_scale, w, w_scale, bias, residual, out_dtype,
                                   channels_first, y)
@@ -929,7 +943,6 @@ def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=N
         out_dtype = y.dtype if y is not None else \
             residual.dtype if residual is not None else torch.float32
     dt = _dtype(out_dtype, "y")
-    dev = a.get_device()
     shape = (N, M) if channels_first else (M, N) if a.dim() == 2 else (*a.shape[:-1], N)
     if y is None:
         y = a.new_empty(shape, dtype=out_dtype)
@@ -948,9 +961,11 @@ def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=N
         bp = _vec(bias, N, "bias")
     if w.get_device() != dev or a_scale.get_device() != dev or w_scale.get_device() != dev:
         _one_device(dev, w, a_scale, w_scale)
-    _check(lib().bv_int8_matmul(ap, as_, _vec(a_scale, M, "a_scale"), wp, ws,
-                                _vec(w_scale, N, "w_scale"), bp, M, N, K, rp, rs, yp, ys, dt,
-                                1 if channels_first else 0, _raw_stream(dev)))
+    st = (_LIB or lib()).bv_int8_matmul(ap, as_, _vec(a_scale, M, "a_scale"), wp, ws,
+                                        _vec(w_scale, N, "w_scale"), bp, M, N, K, rp, rs, yp, ys,
+                                        dt, 1 if channels_first else 0, _raw_stream(dev))
+    if st:
+        _check(st)
     return y
 
 
@@ -978,7 +993,8 @@ class TokenFrontEnd:
         Cout = self.w.shape[0]
         if D != self.w.shape[1]:
             raise BVError(2, f"x [..., {D}], weight {tuple(self.w.shape)}")
-        if not _here(stream, x):
+        dev = x.get_device()
+        if not _here(stream, dev):
             with _On(stream, x):
                 return self(x, residual, by_side, z, workspace)
         shape = (S, Cout, T) if by_side else (Cout, S, T)
@@ -991,7 +1007,6 @@ class TokenFrontEnd:
             raise BVError(2, last_error())
         if workspace is None:
             workspace = x.new_empty(need // 4 + 64, dtype=torch.float32)
-        dev = x.get_device()
         _one_device(dev, self.w, self.bias, z, workspace)
         xp, xs, rp, rs, _, _, gp, gdt, rows, cols, dt = _norm_args(x, self.gain, residual, None,
                                                                      dev)

@@ -272,12 +272,13 @@ SHAPES = [(1, 1, 1), (1, 5, 3), (2, 16, 32), (1, 128, 64), (3, 33, 127), (16, 25
           (1, 40000, 64), (20000, 1, 48), (4100, 260, 4096)]
 
 
-@pytest.mark.parametrize("pad", [True, False])
+@pytest.mark.parametrize("pad", ["both", "a", "w", "none"])
 @pytest.mark.parametrize("cf", [False, True])
 @pytest.mark.parametrize("M,N,K", SHAPES)
 def test_product_matches_definition(nat, M, N, K, cf, pad):
+    """pad: the operands whose rows start on 16 bytes whatever K is."""
     g = gen(M * 31 + N * 7 + K)
-    a, w = int8(g, M, K, pad), int8(g, N, K, pad)
+    a, w = int8(g, M, K, pad in ("both", "a")), int8(g, N, K, pad in ("both", "w"))
     sa, sw = (torch.rand(n, device="cuda", generator=g) * 0.01 + 1e-4 for n in (M, N))
     bias = randn(g, N)
     y = nat.bv_int8_matmul(a, sa, w, sw, bias=bias, channels_first=cf)
@@ -322,6 +323,18 @@ def test_product_strided_output(nat, dtype, cf, M, N, K, oy, py):
     outside = torch.ones_like(yb, dtype=torch.bool)
     outside[:R, oy:oy + C] = False
     assert (yb[outside] == 7.0).all()
+
+
+@pytest.mark.parametrize("off_a,off_w", [(0, 1), (3, 0), (5, 13), (8, 4)])
+@pytest.mark.parametrize("M,N,K", [(1, 70, 200), (4, 300, 512), (40, 60, 300), (300, 500, 130)])
+def test_product_operands_inside_wider_rows(nat, M, N, K, off_a, off_w):
+    """Operands that start anywhere; the bytes around them are not theirs."""
+    g = gen(M + N + K + off_a)
+    a, w = int8(g, M, K + 20, False)[:, off_a:off_a + K], int8(g, N, K + 33, False)[:, off_w:off_w + K]
+    sa, sw = (torch.rand(n, device="cuda", generator=g) * 0.01 for n in (M, N))
+    for cf in (False, True):
+        y = nat.bv_int8_matmul(a, sa, w, sw, channels_first=cf)
+        check_product(a, sa, w, sw, None, None, y, torch.float32, cf)
 
 
 def test_product_adds_in_place(nat):
