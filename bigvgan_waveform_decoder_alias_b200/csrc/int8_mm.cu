@@ -322,12 +322,13 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t bars[2 * TILE_MAX_STAGES + 1];
+  __shared__ uint64_t bars[3 * TILE_MAX_STAGES + 1];
   __shared__ Ctl ctl;
   __shared__ __align__(16) float cs[NT], cb[NT];  // the tile's columns' scales and biases
   const unsigned bar_full = smem_u32(&bars[0]);
   const unsigned bar_empty = smem_u32(&bars[TILE_MAX_STAGES]);
-  const unsigned bar_done = smem_u32(&bars[2 * TILE_MAX_STAGES]);
+  const unsigned bar_copied = smem_u32(&bars[2 * TILE_MAX_STAGES]);
+  const unsigned bar_done = smem_u32(&bars[3 * TILE_MAX_STAGES]);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)(blockIdx.x % (unsigned)split), tile = (int)(blockIdx.x / (unsigned)split);
   const int row0 = tile % tiles_r * BR, col0 = tile / tiles_r * NT;
@@ -341,7 +342,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
     if (!COPY_C) prefetch_map(&map_c);
     ctl.abort = 0;
     for (int s = 0; s < stages; ++s) {
-      mbar_init(bar_full + 8 * s, (TMA ? 1 : 0) + (COPY ? COPY_WARPS : 0));
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_copied + 8 * s, COPY_WARPS);
       mbar_init(bar_empty + 8 * s, 1);
     }
     mbar_init(bar_done, 1);
@@ -386,7 +388,9 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   } else if (warp == 1 && lane == 0) {
     for (int c = 0; c < n; ++c) {
       const int s = c % stages;
-      if (!mbar_wait(bar_full + 8 * s, (c / stages) & 1, wc, 302)) break;
+      const unsigned phase = (unsigned)(c / stages) & 1u;
+      if (TMA && !mbar_wait(bar_full + 8 * s, phase, wc, 302)) break;
+      if (COPY && !mbar_wait(bar_copied + 8 * s, phase, wc, 305)) break;
       asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
       const unsigned at = smem_u32(smem + s * STAGE);
       const uint64_t da = sw128_desc(at), db = sw128_desc(at + BR * BK);
@@ -434,7 +438,7 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_full + 8 * s);
+      if (lane == 0) mbar_arrive(bar_copied + 8 * s);
     }
   }
   __syncwarp();

@@ -549,3 +549,40 @@ def test_timing_classes(nat):
         nat.timing(False)
         nat.timing_reset()
     assert {"rms_norm", "quantize_rows", "int8_matmul"} <= set(got)
+
+
+def _status(nat):
+    import ctypes
+    return nat.lib().bv_sync_status(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+
+
+@pytest.mark.parametrize("call", ["pair", "tile", "split", "copied", "copied_split", "rows"])
+def test_bounded_waits_report_and_leave_the_context_usable(nat, call):
+    """The bounded waits made to run out at once by the library's testing hook:
+    the status word says so, and the same call at the default limit is right."""
+    g = gen(16)
+    M, N, K, pad = {"pair": (600, 4096, 640, True), "tile": (100, 300, 640, True),
+                    "split": (20, 256, 4096, True), "copied": (100, 300, 650, False),
+                    "copied_split": (20, 256, 4090, False), "rows": (700, 0, 1024, True)}[call]
+    if call == "rows":
+        x = randn(g, M, K)
+        run = lambda: nat.bv_rms_norm(x)  # noqa: E731
+    else:
+        a, w = int8(g, M, K), int8(g, N, K, pad)
+        sa, sw = (torch.rand(n, device="cuda", generator=g) * 0.01 for n in (M, N))
+        run = lambda: nat.bv_int8_matmul(a, sa, w, sw)  # noqa: E731
+    run()
+    assert _status(nat) == 0
+    nat.set_wait_limit(0)
+    try:
+        run()
+        st = _status(nat)
+    finally:
+        nat.set_wait_limit(-1)
+    assert st == 5, st  # BV_ERR_TIMEOUT
+    y = run()
+    assert _status(nat) == 0
+    if call == "rows":
+        check_norm(x, None, None, 1e-6, y, None)
+    else:
+        check_product(a, sa, w, sw, None, None, y, torch.float32, False)
