@@ -720,7 +720,8 @@ class BweTail:
 #
 # These are called once a layer and token, where the host's time counts: the
 # common case (contiguous tensors on the current device, its current stream)
-# takes the short way through each check.
+# takes the short way through each check.  A call whose stream or device is
+# another one enters it (_On) and calls itself.
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -748,7 +749,7 @@ def _rows(t: torch.Tensor, name: str):
 
 
 def _vec(t: torch.Tensor, n: int, name: str, dtype=torch.float32):
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise BVError(1, f"{name} must be a contiguous {dtype} tensor of {n} values")
     return t.data_ptr()
 
@@ -775,12 +776,6 @@ class _On:
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
             c.__exit__(*exc)
-
-
-def _here(stream, dev) -> bool:
-    """Does a call on a tensor of device `dev` (-1: host) run on the current device and
-    stream as it is?"""
-    return stream is None and dev >= 0 and dev == _current_device()
 
 
 def _one_device(dev, *tensors):
@@ -819,7 +814,7 @@ def _dtype(dtype, name) -> int:
 
 def _norm_args(x, gain, residual, h, dev):
     """The leading arguments of both norms (rows, cols last but one)."""
-    dtype = x.dtype
+    dtype, shape = x.dtype, x.shape
     dt = DTYPES.get(dtype)
     if dt is None:
         raise BVError(1, f"x of type {dtype}")
@@ -827,9 +822,16 @@ def _norm_args(x, gain, residual, h, dev):
     rp = hp = gp = None
     rs = hs = gdt = 0
     if residual is not None:
-        rp, rs = _same_rows(residual, x, cols, dev, "residual")
+        if residual.is_contiguous() and residual.dtype is dtype and residual.shape == shape and \
+                residual.get_device() == dev:
+            rp, rs = residual.data_ptr(), cols
+        else:
+            rp, rs = _same_rows(residual, x, cols, dev, "residual")
     if h is not None:
-        hp, hs = _same_rows(h, x, cols, dev, "h")
+        if h.is_contiguous() and h.dtype is dtype and h.shape == shape and h.get_device() == dev:
+            hp, hs = h.data_ptr(), cols
+        else:
+            hp, hs = _same_rows(h, x, cols, dev, "h")
     if gain is not None:
         gdt = DTYPES.get(gain.dtype)
         if gdt is None or gain.numel() != cols or not gain.is_contiguous() or \
@@ -855,7 +857,7 @@ def bv_rms_norm(x, gain=None, eps=1e-6, residual=None, h=None, y=None, stream=No
     gain [cols].  Returns y, with a residual (y, h), h = x + residual in x's
     type; h may be given, and may be x or the residual itself."""
     dev = x.get_device()
-    if not _here(stream, dev):
+    if stream is not None or dev < 0 or dev != _current_device():
         with _On(stream, x):
             return bv_rms_norm(x, gain, eps, residual, h, y)
     if residual is not None and h is None:
@@ -895,7 +897,7 @@ def bv_rms_norm_int8(x, gain=None, eps=1e-6, residual=None, h=None, q=None, scal
     """bv_rms_norm with 8-bit rows: (q int8 [..., cols], scale f32 [...]) with
     y = q scale, and h as a third with a residual."""
     dev = x.get_device()
-    if not _here(stream, dev):
+    if stream is not None or dev < 0 or dev != _current_device():
         with _On(stream, x):
             return bv_rms_norm_int8(x, gain, eps, residual, h, q, scale)
     if residual is not None and h is None:
@@ -913,7 +915,7 @@ def bv_quantize_rows(x, q=None, scale=None, stream=None):
     """The rows of x [..., cols] in 8 bits: (q int8 [..., cols], scale f32
     [...]); tokens [M, K] or a weight [N, K] for bv_int8_matmul."""
     dev = x.get_device()
-    if not _here(stream, dev):
+    if stream is not None or dev < 0 or dev != _current_device():
         with _On(stream, x):
             return bv_quantize_rows(x, q, scale)
     dt = _dtype(x.dtype, "x")
@@ -929,11 +931,11 @@ def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=N
     [N]): y [..., N], or with channels_first [N, tokens].  out_dtype: f32 (the
     default), bf16 or f16; y's or the residual's where one is given."""
     dev = a.get_device()
-    if not _here(stream, dev):
+    if stream is not None or dev < 0 or dev != _current_device():
         with _On(stream, a):
             return bv_int8_matmul(a, a_scale, w, w_scale, bias, residual, out_dtype,
                                   channels_first, y)
-    if a.dtype != torch.int8 or w.dtype != torch.int8:
+    if a.dtype is not torch.int8 or w.dtype is not torch.int8:
         raise BVError(1, "a and w must be int8")
     ap, as_, M, K = _rows(a, "a")
     wp, ws, N, Kw = _rows(w, "w")
@@ -942,25 +944,26 @@ def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=N
     if out_dtype is None:
         out_dtype = y.dtype if y is not None else \
             residual.dtype if residual is not None else torch.float32
-    dt = _dtype(out_dtype, "y")
+    dt = DTYPES.get(out_dtype)
+    if dt is None:
+        raise BVError(1, f"y of type {out_dtype}")
     shape = (N, M) if channels_first else (M, N) if a.dim() == 2 else (*a.shape[:-1], N)
     if y is None:
         y = a.new_empty(shape, dtype=out_dtype)
         yp, ys = y.data_ptr(), shape[-1]
     else:
-        if y.shape != shape or y.dtype != out_dtype:
+        if y.shape != shape or y.dtype is not out_dtype:
             raise BVError(2, f"y must be {out_dtype} of shape {tuple(shape)}")
         _one_device(dev, y)
         yp, ys, _, _ = _rows(y, "y")
     rp, rs, bp = None, 0, None
     if residual is not None:
-        _one_device(dev, residual)
-        rp, rs, _, _ = _rows(_like(residual, y, out_dtype, "residual"), "residual")
+        rp, rs = _same_rows(residual, y, shape[-1], dev, "residual")
     if bias is not None:
-        _one_device(dev, bias)
         bp = _vec(bias, N, "bias")
-    if w.get_device() != dev or a_scale.get_device() != dev or w_scale.get_device() != dev:
-        _one_device(dev, w, a_scale, w_scale)
+    if w.get_device() != dev or a_scale.get_device() != dev or w_scale.get_device() != dev or \
+            (bias is not None and bias.get_device() != dev):
+        _one_device(dev, w, a_scale, w_scale, bias)
     st = (_LIB or lib()).bv_int8_matmul(ap, as_, _vec(a_scale, M, "a_scale"), wp, ws,
                                         _vec(w_scale, N, "w_scale"), bp, M, N, K, rp, rs, yp, ys,
                                         dt, 1 if channels_first else 0, _raw_stream(dev))
@@ -994,7 +997,7 @@ class TokenFrontEnd:
         if D != self.w.shape[1]:
             raise BVError(2, f"x [..., {D}], weight {tuple(self.w.shape)}")
         dev = x.get_device()
-        if not _here(stream, dev):
+        if stream is not None or dev < 0 or dev != _current_device():
             with _On(stream, x):
                 return self(x, residual, by_side, z, workspace)
         shape = (S, Cout, T) if by_side else (Cout, S, T)
