@@ -189,19 +189,10 @@ struct Piece {
     }
   }
   __device__ __forceinline__ uint4 bytes() const {
-    unsigned w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (off & 8) {
-#pragma unroll
-      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (off & 4) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    unsigned v[4];
+    const uint4 w = bytes_from(a, b, off);
+    unsigned v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[i] = __funnelshift_r(w[i], w[i + 1], 8 * (off & 3));
       const int left = n - 4 * i;  // bytes of this word inside K
       if (left < 4) v[i] = left <= 0 ? 0u : v[i] & (0xffffffffu >> (32 - 8 * left));
     }

@@ -183,50 +183,124 @@ struct Lay {
   }
 };
 
-// Group i of a row straight from memory (zero outside the row).  Plain loads:
-// the row may be overwritten by this kernel.
+// Group i of a row straight from memory (zero outside the row); [lo, hi) is the
+// whole tensor, so a row's ends are read with their neighbours' values unless
+// those lie outside it.  Plain loads: the row may be overwritten by this kernel.
 template <typename T, int VEC, bool RAGGED>
-__device__ __forceinline__ Pack<T, VEC> load_group(const T *row, const Lay<VEC, RAGGED> &l, int i) {
+__device__ __forceinline__ Pack<T, VEC> load_group(const T *row, const Lay<VEC, RAGGED> &l, int i,
+                                                   const T *lo, const T *hi) {
   Pack<T, VEC> p;
-  if (l.whole(i)) {
-    p = *reinterpret_cast<const Pack<T, VEC> *>(row + l.first(i));
+  const int first = l.first(i);
+  const T *at = row + first;
+  if (RAGGED ? l.some(i) && at >= lo && at + VEC <= hi : l.whole(i)) {
+    p = *reinterpret_cast<const Pack<T, VEC> *>(at);
+    if (RAGGED && !l.whole(i)) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e < -first || e >= l.cols - first) p.v[e] = from_f32<T>(0.0f);
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-      p.v[e] = RAGGED && l.has(i, e) ? row[l.first(i) + e] : from_f32<T>(0.0f);
+      p.v[e] = RAGGED && l.has(i, e) ? at[e] : from_f32<T>(0.0f);
   }
   return p;
+}
+
+// Bytes [lo, hi) of w to the 16-byte aligned `to`, in pieces of 8, 4, 2 and 1
+// bytes where one end is 0 or 16 (of a row's two ends in one group, value by value).
+template <int SIZE>
+__device__ __forceinline__ void store_part(char *to, const uint4 &w, int lo, int hi) {
+  if (lo == 0) {
+    int at = 0;
+    if (hi & 8) {
+      *reinterpret_cast<uint2 *>(to) = make_uint2(w.x, w.y);
+      at = 8;
+    }
+    if (hi & 4) {
+      *reinterpret_cast<unsigned *>(to + at) = at ? w.z : w.x;
+      at += 4;
+    }
+    if (SIZE == 2 && (hi & 2)) {
+      const unsigned v = at & 8 ? (at & 4 ? w.w : w.z) : (at & 4 ? w.y : w.x);
+      *reinterpret_cast<unsigned short *>(to + at) = (unsigned short)v;
+    }
+  } else if (hi == 16) {
+    const int n = 16 - lo;
+    int at = 16;
+    if (n & 8) {
+      *reinterpret_cast<uint2 *>(to + 8) = make_uint2(w.z, w.w);
+      at = 8;
+    }
+    if (n & 4) {
+      at -= 4;
+      *reinterpret_cast<unsigned *>(to + at) = at == 12 ? w.w : w.y;
+    }
+    if (SIZE == 2 && (n & 2)) {
+      at -= 2;
+      const unsigned v = at & 8 ? (at & 4 ? w.w : w.z) : (at & 4 ? w.y : w.x);
+      *reinterpret_cast<unsigned short *>(to + at) = (unsigned short)(v >> 16);
+    }
+  } else {
+    const unsigned v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 16; i += SIZE)
+      if (i >= lo && i < hi) {
+        if (SIZE == 2) *reinterpret_cast<unsigned short *>(to + i) = (unsigned short)(v[i / 4] >> (8 * (i & 2)));
+        else *reinterpret_cast<unsigned *>(to + i) = v[i / 4];
+      }
+  }
 }
 template <typename T, int VEC, bool RAGGED>
 __device__ __forceinline__ void store_group(T *row, const Lay<VEC, RAGGED> &l, int i,
                                             const Pack<T, VEC> &o) {
+  const int first = l.first(i);
   if (l.whole(i)) {
-    *reinterpret_cast<Pack<T, VEC> *>(row + l.first(i)) = o;
-  } else if (RAGGED) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (l.has(i, e)) row[l.first(i) + e] = o.v[e];
+    *reinterpret_cast<Pack<T, VEC> *>(row + first) = o;
+  } else if (RAGGED && l.some(i)) {
+    constexpr int ES = (int)sizeof(T);
+    store_part<ES>(reinterpret_cast<char *>(row + first), *reinterpret_cast<const uint4 *>(&o),
+                   ES * max(0, -first), ES * min(VEC, l.cols - first));
   }
 }
-// Gain of group i.  Only its elements' alignment is known where RAGGED.
+// Gain of group i.  Only its elements' alignment is known where RAGGED: there the
+// two 16-byte words that hold it are read and shifted.
 template <typename G, int VEC, bool RAGGED>
 __device__ __forceinline__ Pack<G, VEC> load_gain(const G *gain, const Lay<VEC, RAGGED> &l, int i) {
   Pack<G, VEC> g;
   if constexpr (!RAGGED) {
     if (l.whole(i)) g = *reinterpret_cast<const Pack<G, VEC> *>(gain + l.first(i));
+    return g;
   } else {
+    const int first = l.first(i);
+    if constexpr (sizeof(G) * VEC == 16) {
+      const char *p = reinterpret_cast<const char *>(gain + first);
+      const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+      const char *w = p - off;
+      if (l.whole(i) && w >= reinterpret_cast<const char *>(gain) &&
+          w + 32 <= reinterpret_cast<const char *>(gain + l.cols)) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(w));
+        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w) + 1);
+        *reinterpret_cast<uint4 *>(&g) = bytes_from(a, b, off);
+        return g;
+      }
+    } else if (l.whole(i)) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g.v[e] = __ldg(gain + first + e);
+      return g;
+    }
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-      g.v[e] = l.has(i, e) ? __ldg(gain + l.first(i) + e) : from_f32<G>(0.0f);
+      g.v[e] = l.has(i, e) ? __ldg(gain + first + e) : from_f32<G>(0.0f);
+    return g;
   }
-  return g;
 }
 
 // Writes a group's VEC 8-bit values, the bytes of `word`.  q's rows start on
 // VEC bytes, so where RAGGED the group that q stores whole, [c0, c0 + VEC), is
 // the upper part of this thread's word and the lower part of the next one's;
-// where a warp or a row ends the parts go out by bytes.  Every lane of the warp
-// calls this.
+// where a warp or a row ends the parts go out in smaller pieces.  Every lane of
+// the warp calls this.
 template <int VEC, bool RAGGED>
 __device__ __forceinline__ void store_q(int8_t *q, uint64_t word, const Lay<VEC, RAGGED> &l, int i) {
   const int c0 = VEC * (l.tid + i * l.tpr);
@@ -239,21 +313,46 @@ __device__ __forceinline__ void store_q(int8_t *q, uint64_t word, const Lay<VEC,
   } else {
     const int lane = threadIdx.x & 31, m = l.m;
     const uint64_t next = __shfl_down_sync(0xffffffffu, word, 1);
-    const bool low = lane == 0 || l.tid == 0, high = lane == 31 || l.tid == l.tpr - 1;
-    if (low) {
+    const bool high = lane == 31 || l.tid == l.tpr - 1;
+    if (m > 0 && (lane == 0 || l.tid == 0) && c0 > 0) {
+      // the lower part, [c0 - m, c0): the lane that stores it whole is not here
+      if (c0 <= l.cols) {
+        int at = c0;
+        uint64_t w = word << (8 * (8 - m));  // its last byte on top
+        if (m & 4) {
+          at -= 4;
+          *reinterpret_cast<unsigned *>(q + at) = (unsigned)(w >> 32);
+          w <<= 32;
+        }
+        if (m & 2) {
+          at -= 2;
+          *reinterpret_cast<unsigned short *>(q + at) = (unsigned short)(w >> 48);
+          w <<= 16;
+        }
+        if (m & 1) q[at - 1] = (int8_t)(w >> 56);
+      } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (e < m && l.has(i, e)) q[c0 - m + e] = (int8_t)(word >> (8 * e));
+        for (int e = 0; e < VEC; ++e)
+          if (e < m && c0 - m + e < l.cols) q[c0 - m + e] = (int8_t)(word >> (8 * e));
+      }
     }
-    const uint64_t all =
-        m == 0 ? word : (word >> (8 * m)) | (high ? 0 : next << (8 * (VEC - m)));
+    uint64_t all = m == 0 ? word : (word >> (8 * m)) | (high ? 0 : next << (8 * (VEC - m)));
     const int n = min(l.cols - c0, high ? VEC - m : VEC);  // values of [c0, c0 + VEC) in hand
     if (n >= VEC) {
       whole_store(all);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (e < n) q[c0 + e] = (int8_t)(all >> (8 * e));
+    } else if (n > 0) {
+      int8_t *to = q + c0;
+      if (n & 4) {
+        *reinterpret_cast<unsigned *>(to) = (unsigned)all;
+        to += 4;
+        all >>= 32;
+      }
+      if (n & 2) {
+        *reinterpret_cast<unsigned short *>(to) = (unsigned short)all;
+        to += 2;
+        all >>= 16;
+      }
+      if (n & 1) *to = (int8_t)all;
     }
   }
 }
@@ -367,6 +466,8 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 128) rows_kernel(NormArgs a, in
   l.tid = BLOCK ? threadIdx.x : (threadIdx.x & (tpr - 1));
   l.cols = a.cols;
   const int per = BLOCK ? 1 : 128 / tpr;  // rows a block
+  const T *x0 = static_cast<const T *>(a.x), *x1 = x0 + (a.rows - 1) * a.xs + a.cols;
+  const T *r0 = static_cast<const T *>(a.residual), *r1 = r0 + (a.rows - 1) * a.rs + a.cols;
   int buf = 0;
   for (int64_t first = blockIdx.x * (int64_t)per; first < a.rows; first += gridDim.x * (int64_t)per) {
     int64_t row = first + (BLOCK ? 0 : threadIdx.x / tpr);
@@ -375,15 +476,15 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 128) rows_kernel(NormArgs a, in
     if (!BLOCK && row >= a.rows) row = a.rows - 1;
     const T *x = static_cast<const T *>(a.x) + row * a.xs;
     const T *r = static_cast<const T *>(a.residual) + row * a.rs;
-    l.m = shift_of<T, VEC>(x);
+    l.m = RAGGED ? shift_of<T, VEC>(x) : 0;
     float2 h[NV][P];
     Pack<G, VEC> g[NV];
     {
       Pack<T, VEC> px[NV], pr[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        px[i] = load_group(x, l, i);
-        if (MODE != kQuant && a.residual) pr[i] = load_group(r, l, i);
+        px[i] = load_group(x, l, i, x0, x1);
+        if (MODE != kQuant && a.residual) pr[i] = load_group(r, l, i, r0, r1);
         if (MODE != kQuant && a.gain) g[i] = load_gain(static_cast<const G *>(a.gain), l, i);
       }
 #pragma unroll
@@ -398,13 +499,14 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 128) rows_kernel(NormArgs a, in
   }
 }
 
-// Many rows, each on whole 16-byte groups: persistent blocks, a row a block,
-// each with a ring of row slots in shared memory that bulk copies fill ahead of
+// Many rows: persistent blocks, a row a block, each with a ring of row slots in shared memory that bulk copies fill ahead of
 // the row in work, so the reads of the next rows are in flight while a row is
 // reduced and written; the gains stay in registers.  (Straight loads wait out
 // each row's latency: 16384 rows of 8192 bf16 values with a residual took 259
 // us from rows_kernel, 173 us = 6.2 TB/s from here; 8192 x 4096 to 8 bits 71
-// and 47 us.)  A slot holds x's row, then the residual's.
+// and 47 us.)  A slot holds the 16-byte pieces that cover x's row, then the
+// residual's; RAGGED rows share pieces with their neighbours, so those at the
+// ends of the tensor's first and last row are left out and read from memory.
 struct Ring {
   int slots;
   int row_bytes;   // one operand
@@ -412,14 +514,14 @@ struct Ring {
 };
 constexpr int kMaxSlots = 3;
 
-template <typename T, typename G, int NV, Mode MODE>
+template <typename T, typename G, int NV, Mode MODE, bool RAGGED>
 __global__ void __launch_bounds__(512)
 stream_rows_kernel(NormArgs a, Ring ring, int *status, long long wait_limit) {
   constexpr int VEC = 16 / (int)sizeof(T), P = VEC / 2;
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ Red red;
   __shared__ uint64_t bars[kMaxSlots];
-  Lay<VEC, false> l;
+  Lay<VEC, RAGGED> l;
   l.tpr = blockDim.x;
   l.tid = threadIdx.x;
   l.m = 0;
@@ -427,15 +529,33 @@ stream_rows_kernel(NormArgs a, Ring ring, int *status, long long wait_limit) {
   const int64_t step = gridDim.x;
   const unsigned full = smem_u32(&bars[0]);
   const bool residual = MODE != kQuant && a.residual;
+  const T *x0 = static_cast<const T *>(a.x), *r0 = static_cast<const T *>(a.residual);
+  // a row whose partial pieces may reach outside its tensor
+  auto at_end = [&](int64_t row, int64_t stride) {
+    return row == 0 || row == a.rows - 1 || stride < VEC;
+  };
+  auto fetch_row = [&](const T *p, bool end, unsigned dst, unsigned bar, bool issue) {
+    uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    uintptr_t hi = lo + (uintptr_t)a.cols * sizeof(T);
+    if constexpr (RAGGED) {
+      const uintptr_t at = lo & ~(uintptr_t)15;  // the slot's first piece
+      lo = end ? (lo + 15) & ~(uintptr_t)15 : at;
+      hi = end ? hi & ~(uintptr_t)15 : (hi + 15) & ~(uintptr_t)15;
+      if (hi <= lo) return 0u;
+      dst += (unsigned)(lo - at);
+    }
+    if (issue) bulk_load(dst, lo, (unsigned)(hi - lo), bar);
+    return (unsigned)(hi - lo);
+  };
   auto fetch = [&](int64_t row, int slot) {  // one thread
     const unsigned dst = smem_u32(ring_smem + slot * ring.slot_bytes), bar = full + 8 * slot;
-    mbar_arrive_tx(bar, (unsigned)ring.slot_bytes);
-    bulk_load(dst, reinterpret_cast<uintptr_t>(static_cast<const T *>(a.x) + row * a.xs),
-              (unsigned)ring.row_bytes, bar);
-    if (residual)
-      bulk_load(dst + ring.row_bytes,
-                reinterpret_cast<uintptr_t>(static_cast<const T *>(a.residual) + row * a.rs),
-                (unsigned)ring.row_bytes, bar);
+    const T *x = x0 + row * a.xs, *r = r0 + row * a.rs;
+    const bool xe = at_end(row, a.xs), re = at_end(row, a.rs);
+    unsigned bytes = fetch_row(x, xe, dst, bar, false);
+    if (residual) bytes += fetch_row(r, re, dst + ring.row_bytes, bar, false);
+    mbar_arrive_tx(bar, bytes);
+    fetch_row(x, xe, dst, bar, true);
+    if (residual) fetch_row(r, re, dst + ring.row_bytes, bar, true);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < ring.slots; ++s) mbar_init(full + 8 * s, 1);
@@ -444,16 +564,20 @@ stream_rows_kernel(NormArgs a, Ring ring, int *status, long long wait_limit) {
     for (int s = 0; s < ring.slots; ++s)
       if (blockIdx.x + s * step < a.rows) fetch(blockIdx.x + s * step, s);
   }
+  // the gains stay in registers (where rows are shifted, as long as m does)
   Pack<G, VEC> g[NV];
-  if (MODE != kQuant && a.gain) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) g[i] = load_gain(static_cast<const G *>(a.gain), l, i);
-  }
+  int gm = -1;
   __syncthreads();
   int buf = 0, slot = 0;
   unsigned parity = 0;
   long long limit = wait_limit;
   for (int64_t row = blockIdx.x; row < a.rows; row += step) {
+    if (RAGGED) l.m = shift_of<T, VEC>(x0 + row * a.xs);
+    if (MODE != kQuant && a.gain && gm != l.m) {
+      gm = l.m;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) g[i] = load_gain(static_cast<const G *>(a.gain), l, i);
+    }
     // A wait that runs out is reported and the copy drained (with its own
     // bound); later waits then only look once.
     bool ok = false;
@@ -464,30 +588,39 @@ stream_rows_kernel(NormArgs a, Ring ring, int *status, long long wait_limit) {
       limit = 1;
     }
     const unsigned char *at = ring_smem + slot * ring.slot_bytes;
-    auto take = [&](int off, int i) {
+    auto take = [&](const T *tensor, int64_t stride, int off, int i) {
       Pack<T, VEC> p;
-      if (l.whole(i)) {
+      const bool whole = l.whole(i);
+      if (whole || (RAGGED && l.some(i) && !at_end(row, stride))) {
         p = *reinterpret_cast<const Pack<T, VEC> *>(at + off + 16 * (l.tid + i * l.tpr));
-      } else {
+        if (!whole) {
+          const int first = l.first(i);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) p.v[e] = from_f32<T>(0.0f);
+          for (int e = 0; e < VEC; ++e)
+            if (e < -first || e >= l.cols - first) p.v[e] = from_f32<T>(0.0f);
+        }
+      } else {
+        const T *p_row = tensor + row * stride;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          p.v[e] = RAGGED && l.has(i, e) ? p_row[l.first(i) + e] : from_f32<T>(0.0f);
       }
       return p;
     };
     float2 h[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const Pack<T, VEC> px = take(0, i);
+      const Pack<T, VEC> px = take(x0, a.xs, 0, i);
 #pragma unroll
       for (int p = 0; p < P; ++p) h[i][p] = get2(px, p);
       if (residual) {
-        const Pack<T, VEC> pr = take(ring.row_bytes, i);
+        const Pack<T, VEC> pr = take(r0, a.rs, ring.row_bytes, i);
 #pragma unroll
         for (int p = 0; p < P; ++p) h[i][p] = add2(h[i][p], get2(pr, p));
       }
     }
     const int64_t next = row + ring.slots * step;
-    finish_row<T, G, NV, true, MODE, false>(a, row, l, h, g, red, buf, [&] {
+    finish_row<T, G, NV, true, MODE, RAGGED>(a, row, l, h, g, red, buf, [&] {
       if (threadIdx.x == 0 && next < a.rows) fetch(next, slot);
     });
     if (++slot == ring.slots) {
@@ -566,14 +699,14 @@ int up32(int v) { return (v + 31) / 32 * 32; }
 constexpr int kSms = 148;
 constexpr int kMaxGroups = 4096;  // 16-byte groups a row that a block's registers hold
 
-template <typename T, typename G, int NV, Mode MODE>
+template <typename T, typename G, int NV, Mode MODE, bool RAGGED>
 bv_status launch_stream(const NormArgs &a, int threads, cudaStream_t st) {
   // Blocks an SM: 1024 threads' worth (8192 x 2048 bf16 to 8 bits: 27.3 us so,
   // 28.0 us with half of them).  Past 256 threads one block with a residual
   // (16384 x 8192 bf16 173 us, two blocks 194 us), else two (8192 x 8192 f32 to
   // 8 bits 53 us, one block 61 us).
   Ring ring;
-  ring.row_bytes = a.cols * (int)sizeof(T);
+  ring.row_bytes = (a.cols * (int)sizeof(T) + (RAGGED ? 30 : 0)) / 16 * 16;
   ring.slot_bytes = ring.row_bytes * (a.residual ? 2 : 1);
   int per_sm = threads <= 256 ? 1024 / threads : a.residual ? 1 : 2;
   per_sm = std::max(1, std::min(per_sm, 200 * 1024 / (2 * ring.slot_bytes)));
@@ -581,10 +714,11 @@ bv_status launch_stream(const NormArgs &a, int threads, cudaStream_t st) {
   int *status = device_status_ptr();
   if (!status) return fail(BV_ERR_CUDA, "rms_norm: status word");
   const size_t smem = (size_t)ring.slots * ring.slot_bytes;
-  auto k = stream_rows_kernel<T, G, NV, MODE>;
+  auto k = stream_rows_kernel<T, G, NV, MODE, RAGGED>;
   // (room beside the kernel's static shared memory too)
   BV_TRY(ensure_dynamic_smem((const void *)k, smem + 2048, "rms_norm smem"));
-  const int64_t blocks = std::min<int64_t>(a.rows, kSms * per_sm);
+  // (RAGGED: in eights, so that a block's rows all have the same m)
+  const int64_t blocks = std::min<int64_t>(a.rows, RAGGED ? kSms * per_sm / 8 * 8 : kSms * per_sm);
   k<<<(unsigned)blocks, threads, smem, st>>>(a, ring, status, wait_limit());
   return BV_OK;
 }
@@ -611,21 +745,23 @@ bv_status launch_vec(const NormArgs &a, cudaStream_t st) {
     return launch_direct<T, G, 2, false, MODE, RAGGED>(a, lanes, st);
   }
   // Two blocks an SM and more go through the ring (300 x 4096 bf16 to 8 bits:
-  // 5.3 us, 5.7 us without it; 1200 x 4096: 9.7 and 13.8 us).  Ragged rows
-  // spend their time at the rows' ends, ring or not (8192 x 1501 bf16 to 8
-  // bits: 47 us through one, 40 us without).
+  // 5.3 us, 5.7 us without it; 1200 x 4096: 9.7 and 13.8 us; ragged 8192 x 4097
+  // f32 107 and 128 us).  Ragged rows spend their time on the rows' ends, so
+  // there fewer threads take more groups and more rows are in work at a time
+  // (8192 x 8191 bf16 157 us with 160 threads, 172 us with 288).
   const bool many = a.rows >= 2 * kSms;
-  if constexpr (!RAGGED) {
-    if (many) {
-      if (groups <= 1024) return launch_stream<T, G, 2, MODE>(a, up32((groups + 1) / 2), st);
-      if (groups <= 2048) return launch_stream<T, G, 4, MODE>(a, up32((groups + 3) / 4), st);
-      return launch_stream<T, G, 8, MODE>(a, up32((groups + 7) / 8), st);
-    }
+  if (many) {
+    const int nv = RAGGED ? (groups <= 256 ? 2 : groups <= 1024 ? 4 : 8)
+                          : (groups <= 1024 ? 2 : groups <= 2048 ? 4 : 8);
+    const int threads = up32((groups + nv - 1) / nv);
+    if (nv == 2) return launch_stream<T, G, 2, MODE, RAGGED>(a, threads, st);
+    if (nv == 4) return launch_stream<T, G, 4, MODE, RAGGED>(a, threads, st);
+    return launch_stream<T, G, 8, MODE, RAGGED>(a, threads, st);
   }
   // Few rows: one group a thread, as long as a block has threads (one row of
   // 4096 bf16 values: 2.6 us with 512 threads, 3.0 us with 256).
-  if (!many && groups <= 1024) return launch_direct<T, G, 1, true, MODE, RAGGED>(a, up32(groups), st);
-  if (groups <= (many ? 1024 : 2048))
+  if (groups <= 1024) return launch_direct<T, G, 1, true, MODE, RAGGED>(a, up32(groups), st);
+  if (groups <= 2048)
     return launch_direct<T, G, 2, true, MODE, RAGGED>(a, up32((groups + 1) / 2), st);
   return launch_direct<T, G, 4, true, MODE, RAGGED>(a, up32((groups + 3) / 4), st);
 }
