@@ -60,7 +60,9 @@ def parse():
                          "frontend:CxSxT:Cout (latent de-normalisation + dec_in) | "
                          "dav:FRAMES (the Music-3 DAV decoder on a stereo latent) | "
                          "bwe:FRAMES (the LTX bandwidth-extension tail on FRAMES mel hops of "
-                         "stereo 16 kHz input)")
+                         "stereo 16 kHz input) | "
+                         "rmsnorm8:ROWSxCOLS (bf16 rows with a residual to 8 bits) | "
+                         "int8mm:MxNxK (8-bit product, bf16 out)")
     return ap.parse_args()
 
 
@@ -97,6 +99,20 @@ def run_case(args):
             work = frames * sp.hop / sp.in_rate
         unit = "audio_s/s"
         return _time_case(args, native, fn, work, unit)
+    if kind == "rmsnorm8":
+        m, n = (int(v) for v in shape.split("x"))
+        x, r = (torch.from_numpy(s.normal((m, n))).cuda().to(torch.bfloat16) for _ in range(2))
+        g = torch.ones(n, device="cuda", dtype=torch.bfloat16)
+        q, sc, h = native.bv_rms_norm_int8(x, g, residual=r)
+        fn = lambda: native.bv_rms_norm_int8(x, g, residual=r, h=h, q=q, scale=sc)  # noqa: E731
+        return _time_case(args, native, fn, 7.0 * m * n, "GB/s")
+    if kind == "int8mm":
+        m, n, k = (int(v) for v in shape.split("x"))
+        a, sa = native.bv_quantize_rows(torch.from_numpy(s.normal((m, k))).cuda())
+        w, sw = native.bv_quantize_rows(torch.from_numpy(s.normal((n, k))).cuda())
+        y = torch.empty((m, n), device="cuda", dtype=torch.bfloat16)
+        fn = lambda: native.bv_int8_matmul(a, sa, w, sw, y=y)  # noqa: E731
+        return _time_case(args, native, fn, 2.0 * m * n * k, "TFLOP/s")
     B, C, T = (int(v) for v in shape.split("x"))
     x = torch.from_numpy(s.normal((B, C, T))).cuda()
     if kind == "frontend":

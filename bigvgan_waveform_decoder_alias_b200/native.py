@@ -665,6 +665,14 @@ class DavDecoder:
         return y
 
 
+    def decode_tokens(self, x: torch.Tensor, front: "TokenFrontEnd", residual=None, y=None,
+                      workspace=None, stream=None) -> torch.Tensor:
+        """Hidden states x [B, frames, cols] of a model -> waveform, as
+        Decoder.decode_tokens."""
+        with _On(stream, x):
+            return self.decode(front(x, residual, by_side=True), y, workspace)
+
+
 # ----------------------------------------------- bandwidth-extension tail
 
 

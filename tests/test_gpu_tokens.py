@@ -513,6 +513,58 @@ def test_decode_tokens(nat, oracle, with_front_end):
     assert err < 1e-4  # the decoder's own tolerance
 
 
+def test_decode_tokens_music(nat):
+    """The DAV decoder takes the front end's latents by side."""
+    from bigvgan_waveform_decoder_alias_b200 import synth
+    geo = synth.MUSIC3_DAV
+    s = synth.NormalStream(78)
+    dec = nat.DavDecoder(geo, synth.draw_dav_params(s, geo))
+    g = gen(17)
+    front = nat.TokenFrontEnd(None, randn(g, geo.latent_channels, 96) / 10)
+    x, r = randn(g, 2, 4, 96), randn(g, 2, 4, 96)
+    y = dec.decode_tokens(x, front, residual=r)
+    assert y.shape == (2, 1, 4 * geo.hop)
+    assert torch.equal(y, dec.decode(front(x, r, by_side=True)))
+
+
+def test_captured_without_a_call_before():
+    """Shapes whose kernels no call has used yet, captured in a new process
+    after one call of another shape; replays equal eager calls."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from bigvgan_waveform_decoder_alias_b200 import native
+def call(m, n, k, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((m, k), device="cuda", generator=g)
+    w = torch.randint(-128, 128, (n, k), device="cuda", generator=g, dtype=torch.int8)
+    sw = torch.rand(n, device="cuda", generator=g)
+    def f():
+        q, s, h = native.bv_rms_norm_int8(x, residual=x)
+        return native.bv_int8_matmul(q, s, w, sw, out_dtype=torch.bfloat16), h
+    return f
+call(8, 16, 32, 0)()
+torch.cuda.synchronize()
+for i, (m, n, k) in enumerate([(1, 300, 64), (30, 200, 4096), (700, 4096, 256), (600, 5000, 520),
+                               (900, 700, 999), (4, 64, 40000)]):
+    f = call(m, n, k, i)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f()
+    graph.replay()
+    torch.cuda.synchronize()
+    want = f()
+    assert all(torch.equal(a, b) for a, b in zip(out, want)), (m, n, k)
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
 def test_refusals(nat):
     g = gen(14)
     x = randn(g, 4, 64)
