@@ -1,8 +1,11 @@
-"""Build libbv.so (the CUDA library) in-tree with nvcc for sm_100a."""
+"""Build libbv.so (the CUDA library) in-tree with nvcc for sm_100a, and the
+tensor marshalling of its token operators (_tokens, C++ against torch)."""
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,15 +25,42 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+BINDING_SRC = os.path.join(CSRC, "token_binding.cpp")
+BINDING = os.path.join(PKG, "_tokens" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def _older(out, deps):
+    return not os.path.exists(out) or any(os.path.getmtime(d) > os.path.getmtime(out) for d in deps)
+
+
 def _stale():
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+                  glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    if not force and not _older(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "bv.h")]):
+        return BINDING
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"))
+    inc = [os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_path("include"), INCLUDE]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-DTORCH_EXTENSION_NAME=_tokens", *(f"-isystem{d}" for d in inc), BINDING_SRC,
+           "-o", BINDING + ".tmp", "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.check_call(cmd)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_binding(force, verbose)
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")

@@ -1,13 +1,12 @@
 """ctypes binding of libbv.so (the C ABI declared in include/bv.h).
 
-Argument marshalling only: every step of the computation runs in the CUDA
-kernels of libbv.  PyTorch provides device memory and streams.  There is no
+Argument marshalling only (the token operators' in C++, see _tokens): every
+step of the computation runs in the CUDA kernels of libbv.  PyTorch provides device memory and streams.  There is no
 fallback: if libbv.so cannot be loaded, or a call fails, a BVError is raised.
 """
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from typing import Optional, Sequence
 
@@ -552,9 +551,11 @@ class Decoder:
         """Hidden states x [B, frames, cols] of a model -> waveform: the token
         front end into this decoder's latents, then decode().  `workspace`
         is the decode's; the front end takes its own."""
-        with _On(stream, x):
-            z = front(x, residual, by_side=self.cfg.latent_channels == 0)
-            return self.decode(z, y, workspace)
+        if stream is not None:
+            with _on(stream, x):
+                return self.decode_tokens(x, front, residual, y, workspace)
+        z = front(x, residual, by_side=self.cfg.latent_channels == 0)
+        return self.decode(z, y, workspace)
 
     # ------------------------------------------------ units, for sharding
     def tile_count(self, frames: int) -> int:
@@ -669,8 +670,10 @@ class DavDecoder:
                       workspace=None, stream=None) -> torch.Tensor:
         """Hidden states x [B, frames, cols] of a model -> waveform, as
         Decoder.decode_tokens."""
-        with _On(stream, x):
-            return self.decode(front(x, residual, by_side=True), y, workspace)
+        if stream is not None:
+            with _on(stream, x):
+                return self.decode_tokens(x, front, residual, y, workspace)
+        return self.decode(front(x, residual, by_side=True), y, workspace)
 
 
 # ----------------------------------------------- bandwidth-extension tail
@@ -726,211 +729,67 @@ class BweTail:
 
 # --------------------------------------------------------- token operators
 #
-# These are called once a layer and token, where the host's time counts: the
-# common case (contiguous tensors on the current device, its current stream)
-# takes the short way through each check.  A call whose stream or device is
-# another one enters it (_On) and calls itself.
+# Called once a layer and token, where the host's time counts: their tensors
+# are marshalled in C++ (csrc/token_binding.cpp), on the tensors' device and its
+# current stream.
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_TOKENS = None
 
 
-def _rows(t: torch.Tensor, name: str):
-    """(pointer, stride, rows, cols) of t seen as [rows, cols]: consecutive
-    elements within a row, one stride between rows."""
-    if t.is_contiguous() and t.dim() > 0:
-        cols = t.shape[-1]
-        return t.data_ptr(), cols, (t.numel() // cols if cols else math.prod(t.shape[:-1])), cols
-    if t.dim() != 2:
-        if t.dim() == 0:
-            raise BVError(2, f"{name} needs a last dimension")
+def _tokens():
+    """The compiled marshalling of the token operators, bound to libbv."""
+    global _TOKENS
+    if _TOKENS is None:
+        L = lib()
         try:
-            t = t.view(math.prod(t.shape[:-1]), t.shape[-1])
-        except RuntimeError:
-            raise BVError(1, f"{name} has no single stride between its rows") from None
-    rows, cols = t.shape
-    stride, one = t.stride()
-    if one != 1 and cols > 1:
-        raise BVError(1, f"the rows of {name} must be contiguous")
-    return t.data_ptr(), (stride if rows > 1 else cols), rows, cols
+            from . import _tokens as module
+        except ImportError as e:
+            raise BVError(4, f"the token operators' binding is missing ({e}): build it with "
+                             "`python -m bigvgan_waveform_decoder_alias_b200.build_native`") from None
+        names = ("bv_last_error", "bv_rms_norm", "bv_rms_norm_int8", "bv_quantize_rows",
+                 "bv_int8_matmul")
+        module.bind({n: ctypes.cast(getattr(L, n), _fp).value for n in names}, BVError)
+        _TOKENS = module
+    return _TOKENS
 
 
-def _vec(t: torch.Tensor, n: int, name: str, dtype=torch.float32):
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-        raise BVError(1, f"{name} must be a contiguous {dtype} tensor of {n} values")
-    return t.data_ptr()
-
-
-class _On:
-    """Another device or stream for a call: the tensors' device is made current,
-    and new outputs belong to the stream that writes them."""
-
-    def __init__(self, stream, t):
-        if not t.is_cuda:
-            raise BVError(1, "tensors must be CUDA tensors")
-        self.ctx = []
-        if t.device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(t.device))
-        if stream is not None:
-            if stream.device != t.device:
-                raise BVError(1, f"tensors on {t.device}, the stream on {stream.device}")
-            self.ctx.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
-
-
-def _one_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise BVError(1, f"tensors on cuda:{dev} and {t.device}")
-
-
-def _int8_rows(x) -> torch.Tensor:
-    """int8 [..., cols] of x's shape whose rows start on 16 bytes, as
-    bv_int8_matmul reads them fastest: where cols is no multiple of 16, the
-    cols of each padded row (the padding holds nothing)."""
-    cols = x.shape[-1]
-    if cols % 16 == 0:
-        return torch.empty_like(x, dtype=torch.int8) if x.is_contiguous() else \
-            x.new_empty(x.shape, dtype=torch.int8)
-    return x.new_empty((*x.shape[:-1], (cols + 15) // 16 * 16), dtype=torch.int8)[..., :cols]
-
-
-def _new_like(x) -> torch.Tensor:
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
-
-
-def _like(t, x, dtype, name):
-    if t.shape != x.shape or t.dtype != dtype:
-        raise BVError(2, f"{name} must be {dtype} of shape {tuple(x.shape)}")
-    return t
-
-
-def _dtype(dtype, name) -> int:
-    dt = DTYPES.get(dtype)
-    if dt is None:
-        raise BVError(1, f"{name} of type {dtype}")
-    return dt
-
-
-def _norm_args(x, gain, residual, h, dev):
-    """The leading arguments of both norms (rows, cols last but one)."""
-    dtype, shape = x.dtype, x.shape
-    dt = DTYPES.get(dtype)
-    if dt is None:
-        raise BVError(1, f"x of type {dtype}")
-    xp, xs, rows, cols = _rows(x, "x")
-    rp = hp = gp = None
-    rs = hs = gdt = 0
-    if residual is not None:
-        if residual.is_contiguous() and residual.dtype is dtype and residual.shape == shape and \
-                residual.get_device() == dev:
-            rp, rs = residual.data_ptr(), cols
-        else:
-            rp, rs = _same_rows(residual, x, cols, dev, "residual")
-    if h is not None:
-        if h.is_contiguous() and h.dtype is dtype and h.shape == shape and h.get_device() == dev:
-            hp, hs = h.data_ptr(), cols
-        else:
-            hp, hs = _same_rows(h, x, cols, dev, "h")
-    if gain is not None:
-        gdt = DTYPES.get(gain.dtype)
-        if gdt is None or gain.numel() != cols or not gain.is_contiguous() or \
-                gain.get_device() != dev:
-            raise BVError(1, f"gain must be {cols} contiguous values of x's type or f32 on x's device")
-        gp = gain.data_ptr()
-    return xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt
-
-
-def _same_rows(t, x, cols, dev, name):
-    """(pointer, stride) of a tensor of x's shape, type and device."""
-    if t.dtype is not x.dtype or t.shape != x.shape:
-        raise BVError(2, f"{name} must be {x.dtype} of shape {tuple(x.shape)}")
-    if t.get_device() != dev:
-        _one_device(dev, t)
-    if t.is_contiguous():
-        return t.data_ptr(), cols
-    return _rows(t, name)[:2]
+def _on(stream, t):
+    """Context of a call on another stream: new outputs belong to the stream that
+    writes them."""
+    if not t.is_cuda or stream.device != t.device:
+        raise BVError(1, f"tensors on {t.device}, the stream on {stream.device}")
+    return torch.cuda.stream(stream)
 
 
 def bv_rms_norm(x, gain=None, eps=1e-6, residual=None, h=None, y=None, stream=None):
     """Root-mean-square norm of the rows of x [..., cols] (+ residual) times
     gain [cols].  Returns y, with a residual (y, h), h = x + residual in x's
     type; h may be given, and may be x or the residual itself."""
-    dev = x.get_device()
-    if stream is not None or dev < 0 or dev != _current_device():
-        with _On(stream, x):
+    if stream is not None:
+        with _on(stream, x):
             return bv_rms_norm(x, gain, eps, residual, h, y)
-    if residual is not None and h is None:
-        h = _new_like(x)
-    xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h, dev)
-    if y is None:
-        y = _new_like(x)
-        yp, ys = y.data_ptr(), cols
-    else:
-        yp, ys = _same_rows(y, x, cols, dev, "y")
-    st = (_LIB or lib()).bv_rms_norm(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, yp, ys,
-                                     _raw_stream(dev))
-    if st:
-        _check(st)
-    return y if residual is None else (y, h)
-
-
-def _int8_out(x, q, scale, rows, dev):
-    """q and scale of x's rows (new ones where None), q's pointer and stride."""
-    if q is None:
-        q = _int8_rows(x)
-        qp, qs = q.data_ptr(), (x.shape[-1] + 15) // 16 * 16
-    else:
-        _one_device(dev, _like(q, x, torch.int8, "q"))
-        qp, qs, _, _ = _rows(q, "q")
-    if scale is None:
-        scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
-        sp = scale.data_ptr()
-    else:
-        _one_device(dev, scale)
-        sp = _vec(scale, rows, "scale")
-    return q, scale, qp, qs, sp
+    return (_TOKENS or _tokens()).rms_norm(x, gain, eps, residual, h, y)
 
 
 def bv_rms_norm_int8(x, gain=None, eps=1e-6, residual=None, h=None, q=None, scale=None,
                      stream=None):
     """bv_rms_norm with 8-bit rows: (q int8 [..., cols], scale f32 [...]) with
-    y = q scale, and h as a third with a residual."""
-    dev = x.get_device()
-    if stream is not None or dev < 0 or dev != _current_device():
-        with _On(stream, x):
+    y = q scale, and h as a third with a residual.  A new q has rows that start
+    on 16 bytes, as bv_int8_matmul reads them fastest."""
+    if stream is not None:
+        with _on(stream, x):
             return bv_rms_norm_int8(x, gain, eps, residual, h, q, scale)
-    if residual is not None and h is None:
-        h = _new_like(x)
-    xp, xs, rp, rs, hp, hs, gp, gdt, rows, cols, dt = _norm_args(x, gain, residual, h, dev)
-    q, scale, qp, qs, sp = _int8_out(x, q, scale, rows, dev)
-    st = (_LIB or lib()).bv_rms_norm_int8(xp, xs, rp, rs, hp, hs, gp, gdt, eps, rows, cols, dt, qp,
-                                          qs, sp, _raw_stream(dev))
-    if st:
-        _check(st)
-    return (q, scale) if residual is None else (q, scale, h)
+    return (_TOKENS or _tokens()).rms_norm_int8(x, gain, eps, residual, h, q, scale)
 
 
 def bv_quantize_rows(x, q=None, scale=None, stream=None):
     """The rows of x [..., cols] in 8 bits: (q int8 [..., cols], scale f32
     [...]); tokens [M, K] or a weight [N, K] for bv_int8_matmul."""
-    dev = x.get_device()
-    if stream is not None or dev < 0 or dev != _current_device():
-        with _On(stream, x):
+    if stream is not None:
+        with _on(stream, x):
             return bv_quantize_rows(x, q, scale)
-    dt = _dtype(x.dtype, "x")
-    xp, xs, rows, cols = _rows(x, "x")
-    q, scale, qp, qs, sp = _int8_out(x, q, scale, rows, dev)
-    _check(lib().bv_quantize_rows(xp, xs, rows, cols, dt, qp, qs, sp, _raw_stream(dev)))
-    return q, scale
+    return (_TOKENS or _tokens()).quantize_rows(x, q, scale)
 
 
 def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=None,
@@ -938,46 +797,12 @@ def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=N
     """a int8 [..., K] (scales a_scale [...]) times w int8 [N, K] (w_scale
     [N]): y [..., N], or with channels_first [N, tokens].  out_dtype: f32 (the
     default), bf16 or f16; y's or the residual's where one is given."""
-    dev = a.get_device()
-    if stream is not None or dev < 0 or dev != _current_device():
-        with _On(stream, a):
+    if stream is not None:
+        with _on(stream, a):
             return bv_int8_matmul(a, a_scale, w, w_scale, bias, residual, out_dtype,
                                   channels_first, y)
-    if a.dtype is not torch.int8 or w.dtype is not torch.int8:
-        raise BVError(1, "a and w must be int8")
-    ap, as_, M, K = _rows(a, "a")
-    wp, ws, N, Kw = _rows(w, "w")
-    if w.dim() != 2 or K != Kw:
-        raise BVError(2, f"a [..., {K}] times w {tuple(w.shape)}")
-    if out_dtype is None:
-        out_dtype = y.dtype if y is not None else \
-            residual.dtype if residual is not None else torch.float32
-    dt = DTYPES.get(out_dtype)
-    if dt is None:
-        raise BVError(1, f"y of type {out_dtype}")
-    shape = (N, M) if channels_first else (M, N) if a.dim() == 2 else (*a.shape[:-1], N)
-    if y is None:
-        y = a.new_empty(shape, dtype=out_dtype)
-        yp, ys = y.data_ptr(), shape[-1]
-    else:
-        if y.shape != shape or y.dtype is not out_dtype:
-            raise BVError(2, f"y must be {out_dtype} of shape {tuple(shape)}")
-        _one_device(dev, y)
-        yp, ys, _, _ = _rows(y, "y")
-    rp, rs, bp = None, 0, None
-    if residual is not None:
-        rp, rs = _same_rows(residual, y, shape[-1], dev, "residual")
-    if bias is not None:
-        bp = _vec(bias, N, "bias")
-    if w.get_device() != dev or a_scale.get_device() != dev or w_scale.get_device() != dev or \
-            (bias is not None and bias.get_device() != dev):
-        _one_device(dev, w, a_scale, w_scale, bias)
-    st = (_LIB or lib()).bv_int8_matmul(ap, as_, _vec(a_scale, M, "a_scale"), wp, ws,
-                                        _vec(w_scale, N, "w_scale"), bp, M, N, K, rp, rs, yp, ys,
-                                        dt, 1 if channels_first else 0, _raw_stream(dev))
-    if st:
-        _check(st)
-    return y
+    return (_TOKENS or _tokens()).int8_matmul(a, a_scale, w, w_scale, bias, residual, out_dtype,
+                                              channels_first, y)
 
 
 class TokenFrontEnd:
@@ -986,11 +811,14 @@ class TokenFrontEnd:
     bias [Cout] or None."""
 
     def __init__(self, gain, weight, bias=None, eps=1e-6, device="cuda"):
-        weight = torch.as_tensor(weight).to(device)
+        weight = torch.as_tensor(weight).to(device).contiguous()
         if weight.dim() != 2:
             raise BVError(2, f"weight of shape {tuple(weight.shape)}")
         self.w, self.w_scale = bv_quantize_rows(weight)
         self.gain = None if gain is None else torch.as_tensor(gain).to(device).contiguous()
+        if self.gain is not None and (self.gain.dtype not in DTYPES or
+                                      self.gain.numel() != weight.shape[1]):
+            raise BVError(2, f"gain must be {weight.shape[1]} floating-point values")
         self.bias = None if bias is None else \
             torch.as_tensor(bias, dtype=torch.float32).to(device).contiguous()
         self.eps = eps
@@ -998,34 +826,36 @@ class TokenFrontEnd:
     def __call__(self, x, residual=None, by_side=False, z=None, workspace=None, stream=None):
         """x [S, T, cols] (+ residual) -> latents [Cout, S, T], or [S, Cout, T]
         with by_side."""
-        if x.dim() != 3:
-            raise BVError(2, f"x of shape {tuple(x.shape)}")
+        if stream is not None:
+            with _on(stream, x):
+                return self(x, residual, by_side, z, workspace)
+        if x.dim() != 3 or x.dtype not in DTYPES or not x.is_contiguous():
+            raise BVError(1, "x must be contiguous [S, T, cols] of float32, bfloat16 or float16")
         S, T, D = x.shape
         Cout = self.w.shape[0]
         if D != self.w.shape[1]:
             raise BVError(2, f"x [..., {D}], weight {tuple(self.w.shape)}")
-        dev = x.get_device()
-        if stream is not None or dev < 0 or dev != _current_device():
-            with _On(stream, x):
-                return self(x, residual, by_side, z, workspace)
+        if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or
+                                     not residual.is_contiguous()):
+            raise BVError(2, f"residual must be contiguous {x.dtype} of shape {tuple(x.shape)}")
         shape = (S, Cout, T) if by_side else (Cout, S, T)
-        if z is None:
-            z = x.new_empty(shape, dtype=torch.float32)
-        elif tuple(z.shape) != shape:
-            raise BVError(2, f"z must have shape {shape}")
-        need = int(lib().bv_token_front_end_workspace_size(S, T, D))
-        if need == 0:
-            raise BVError(2, last_error())
-        if workspace is None:
-            workspace = x.new_empty(need // 4 + 64, dtype=torch.float32)
-        _one_device(dev, self.w, self.bias, z, workspace)
-        xp, xs, rp, rs, _, _, gp, gdt, rows, cols, dt = _norm_args(x, self.gain, residual, None,
-                                                                     dev)
-        _check(lib().bv_token_front_end(xp, xs, rp, rs, gp, gdt, self.eps, S, T, D, dt,
-                                        self.w.data_ptr(), self.w.stride(0),
-                                        self.w_scale.data_ptr(),
-                                        None if self.bias is None else
-                                        _vec(self.bias, Cout, "bias"), Cout,
-                                        int(bool(by_side)), _ptr(z), _ptr(workspace),
-                                        workspace.numel() * 4, _raw_stream(dev)))
+        for t in (x, residual, z, workspace):
+            if t is not None and t.device != self.w.device:
+                raise BVError(1, f"the front end is on {self.w.device}, a tensor on {t.device}")
+        with torch.cuda.device(x.device):
+            z = torch.empty(shape, device=x.device, dtype=torch.float32) if z is None else z
+            if tuple(z.shape) != shape:
+                raise BVError(2, f"z must have shape {shape}")
+            need = int(lib().bv_token_front_end_workspace_size(S, T, D))
+            if need == 0:
+                raise BVError(2, last_error())
+            if workspace is None:
+                workspace = torch.empty(need // 4 + 64, device=x.device, dtype=torch.float32)
+            _check(lib().bv_token_front_end(
+                x.data_ptr(), D, None if residual is None else residual.data_ptr(), D,
+                None if self.gain is None else self.gain.data_ptr(),
+                0 if self.gain is None else DTYPES[self.gain.dtype], self.eps, S, T, D,
+                DTYPES[x.dtype], self.w.data_ptr(), self.w.stride(0), _ptr(self.w_scale),
+                _ptr(self.bias), Cout, int(bool(by_side)), _ptr(z), _ptr(workspace),
+                workspace.numel() * 4, _stream()))
         return z
