@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p) {
 //
 // Thread 0 loads the stages by TMA.  Where an operand's rows do not start on 16
 // bytes (COPY_R, COPY_C) eight more warps copy that operand instead: aligned
-// words, shifted into place, all of a stage's reads issued before its writes.
+// words, shifted into place.
 
 constexpr int TILE_MAX_STAGES = 12;
 
@@ -400,31 +400,54 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
     constexpr int PASS = 4 * COPY_WARPS;  // rows a pass over the warps
     // rows [first, last) of a stage: BR rows, then NT columns
     constexpr int FIRST = COPY_R ? 0 : BR, LAST = COPY_C ? BR + NT : BR;
+    constexpr int PASSES = COPY ? (LAST - FIRST + PASS - 1) / PASS : 1;
+    // this lane's rows (past the last row of an operand: the last, whose
+    // products no one stores)
+    const int8_t *from[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = FIRST + i * PASS + sub;
+      from[i] = r < BR ? p.r + (int64_t)min(row0 + r, p.rows - 1) * p.rstride
+                       : p.c + (int64_t)min(col0 + r - BR, p.cols - 1) * p.cstride;
+    }
     for (int c = 0; c < n; ++c) {
       const int s = c % stages, u = c / stages;
       if (u > 0 && !warp_wait(bar_empty + 8 * s, (u - 1) & 1, wc, 303)) break;
       unsigned char *at = smem + s * STAGE;
-      const int k = (c0 + c) * BK + 16 * piece;
+      const int k0 = (c0 + c) * BK, k = k0 + 16 * piece;
+      auto put = [&](int i, const uint4 &v) {
+        const int r = FIRST + i * PASS + sub;
+        if (LAST - FIRST == PASSES * PASS || r < LAST)
+          *reinterpret_cast<uint4 *>(at + r * BK + ((piece ^ (r & 7)) << 4)) = v;
+      };
+      if (k0 >= 16 && k0 + BK + 16 <= p.K) {
+        // every word that holds some of the chunk lies inside its row
 #pragma unroll
-      for (int g = FIRST; g < LAST; g += 4 * PASS) {
-        Piece v[4];
+        for (int g = 0; g < PASSES; g += 4) {
+          uint4 lo[4], hi[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = g + i * PASS + sub;
-          if (g + i * PASS >= LAST) continue;
-          if (r < BR) {
-            const bool have = row0 + r < p.rows;
-            v[i].fetch(p.r + (have ? row0 + r : 0) * p.rstride, k, have ? p.K : 0, p.r, rhi);
-          } else {
-            const bool have = r < LAST && col0 + r - BR < p.cols;
-            v[i].fetch(p.c + (have ? col0 + r - BR : 0) * p.cstride, k, have ? p.K : 0, p.c, chi);
+          for (int i = 0; i < 4; ++i) {
+            if (g + i >= PASSES) continue;
+            const int8_t *w = from[g + i] + k;
+            w -= reinterpret_cast<uintptr_t>(w) & 15;
+            lo[i] = __ldg(reinterpret_cast<const uint4 *>(w));
+            hi[i] = __ldg(reinterpret_cast<const uint4 *>(w) + 1);
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = g + i * PASS + sub;
-          if (g + i * PASS < LAST && r < LAST)
-            *reinterpret_cast<uint4 *>(at + r * BK + ((piece ^ (r & 7)) << 4)) = v[i].bytes();
+          for (int i = 0; i < 4; ++i)
+            if (g + i < PASSES)
+              put(g + i, bytes_from(lo[i], hi[i],
+                                    (int)(reinterpret_cast<uintptr_t>(from[g + i]) & 15)));
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < PASSES; ++i) {
+          const int r = FIRST + i * PASS + sub;
+          const int8_t *row = r < BR ? p.r + (int64_t)min(row0 + r, p.rows - 1) * p.rstride
+                                     : p.c + (int64_t)min(col0 + r - BR, p.cols - 1) * p.cstride;
+          Piece v;
+          v.fetch(row, k, p.K, r < BR ? p.r : p.c, r < BR ? rhi : chi);
+          put(i, v.bytes());
         }
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
