@@ -499,14 +499,15 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 128) rows_kernel(NormArgs a, in
   }
 }
 
-// Many rows: persistent blocks, a row a block, each with a ring of row slots in shared memory that bulk copies fill ahead of
-// the row in work, so the reads of the next rows are in flight while a row is
-// reduced and written; the gains stay in registers.  (Straight loads wait out
-// each row's latency: 16384 rows of 8192 bf16 values with a residual took 259
-// us from rows_kernel, 173 us = 6.2 TB/s from here; 8192 x 4096 to 8 bits 71
-// and 47 us.)  A slot holds the 16-byte pieces that cover x's row, then the
-// residual's; RAGGED rows share pieces with their neighbours, so those at the
-// ends of the tensor's first and last row are left out and read from memory.
+// Many rows: persistent blocks, a row a block, each with a ring of row slots
+// in shared memory that bulk copies fill ahead of the row in work, so the reads
+// of the next rows are in flight while a row is reduced and written; the gains
+// stay in registers.  (Straight loads wait out each row's latency: 16384 rows of
+// 8192 bf16 values with a residual took 259 us from rows_kernel, 171 us = 6.3
+// TB/s from here; 8192 x 4096 to 8 bits 71 and 47 us.)  A slot holds the 16-byte
+// pieces that cover x's row, then the residual's; RAGGED rows share pieces with
+// their neighbours, so those at the ends of the tensor's first and last row are
+// left out and read from memory.
 struct Ring {
   int slots;
   int row_bytes;   // one operand
