@@ -607,7 +607,8 @@ bv_status bv_decode_host(const bv_decoder_config *cfg,
  * (0 reads one row for all); rows of outputs must not overlap.  Bytes between
  * the rows of an output are left as they were.  rows = 0 (M = 0) is a valid
  * empty call.  Pointers need their element's alignment only.
- * All are inference operators: the library has no backward passes.
+ * All are inference operators: the library has no backward passes.  Their
+ * bounded device-side waits report through bv_sync_status.
  * ---------------------------------------------------------------------- */
 typedef enum { BV_F32 = 0, BV_BF16 = 1, BV_F16 = 2 } bv_dtype;
 

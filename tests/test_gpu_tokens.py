@@ -140,11 +140,12 @@ def test_many_rows(nat):
 
 
 @pytest.mark.parametrize("cols", [64, 1537, 4096, 20001])
-def test_special_rows(nat, cols):
+@pytest.mark.parametrize("more", [0, 400])
+def test_special_rows(nat, cols, more):
     """Rows of zeros, of one value, tiny and huge rows, infinities and NaN:
-    each shows in its own row only."""
+    each shows in its own row only, alone and ahead of many more rows."""
     g = gen(5)
-    x = randn(g, 9, cols)
+    x = randn(g, 9 + more, cols)
     x[1] = 0
     x[2] = 0
     x[2, cols // 2] = -3.0
@@ -156,7 +157,7 @@ def test_special_rows(nat, cols):
     gain = 1 + 0.3 * randn(g, cols)
     y = nat.bv_rms_norm(x, gain, eps=1e-6)
     h64, rstd, y64 = norm64(x, None, gain, 1e-6)
-    ok = [0, 1, 2, 3, 4, 7, 8]
+    ok = [0, 1, 2, 3, 4, *range(7, 9 + more)]
     # rows 3 and 7 lie below 2^-126 in part: one step of 2^-149 there
     rel = (CHAIN(cols) / 2 + 9) * U
     close(y[ok], y64[ok], y64[ok].abs() * rel + 2.0 ** -149 * 1e4)
@@ -167,7 +168,7 @@ def test_special_rows(nat, cols):
     assert int(q[2].abs().max()) == 127 and int((q[2] != 0).sum()) == 1
     t64 = (x * gain).double()
     a64 = t64.abs().amax(-1, keepdim=True)
-    for row in (0, 3, 4, 7, 8):
+    for row in (0, 3, 4, *range(7, 9 + more, 57)):
         want = torch.round(127 * t64[row] / a64[row])
         # row 3's products are whole multiples of 2^-149: its q follows the
         # rounded products; elsewhere values next to a border may go either way
@@ -189,10 +190,11 @@ def test_norm_of_the_largest_values(nat):
 
 @pytest.mark.parametrize("dtype", ALL)
 @pytest.mark.parametrize("cols,pad", [(64, 64), (100, 3), (256, 8), (1537, 7), (4096, 16)])
-def test_strided_rows_and_what_lies_between(nat, dtype, cols, pad):
+@pytest.mark.parametrize("n", [6, 333])
+def test_strided_rows_and_what_lies_between(nat, dtype, cols, pad, n):
     """Rows of wider matrices; the columns beside them stay as they were."""
     g = gen(cols + pad)
-    n, ld = 6, cols + pad
+    ld = cols + pad
     big = [randn(g, n, ld).to(dtype) for _ in range(4)]
     x, r, h, y = (b[:, pad // 2:pad // 2 + cols] for b in big)
     keep = [b.clone() for b in big]
@@ -214,14 +216,55 @@ def test_strided_rows_and_what_lies_between(nat, dtype, cols, pad):
 
 @pytest.mark.parametrize("cols", [96, 1001, 8192, 40000])
 @pytest.mark.parametrize("over", ["x", "residual"])
-def test_sum_in_place(nat, cols, over):
+@pytest.mark.parametrize("rows", [5, 700])
+def test_sum_in_place(nat, cols, over, rows):
     g = gen(cols)
-    x, r = randn(g, 5, cols).to(torch.bfloat16), randn(g, 5, cols).to(torch.bfloat16)
+    x, r = randn(g, rows, cols).to(torch.bfloat16), randn(g, rows, cols).to(torch.bfloat16)
     kx, kr = x.clone(), r.clone()
     y, h = nat.bv_rms_norm(x, None, residual=r, h=x if over == "x" else r)
     assert h is (x if over == "x" else r)
     check_norm(kx, kr, None, 1e-6, y, h)
     assert torch.equal(r if over == "x" else x, kr if over == "x" else kx)
+
+
+@pytest.mark.parametrize("cols", [200, 1001, 1024])
+@pytest.mark.parametrize("dtype", ALL)
+def test_many_broadcast_rows(nat, cols, dtype):
+    """One row read for all (stride 0), as x and as the residual."""
+    g = gen(cols)
+    x, r = randn(g, 400, cols).to(dtype), randn(g, 1, cols).to(dtype).expand(400, cols)
+    y, h = nat.bv_rms_norm(x, None, residual=r)
+    check_norm(x, r, None, 1e-6, y, h)
+    y, h = nat.bv_rms_norm(r, None, residual=x)
+    check_norm(r, x, None, 1e-6, y, h)
+    q, _ = nat.bv_quantize_rows(r)
+    np.testing.assert_array_equal(q.cpu().numpy(), expected_q(r, None, None)[0])
+
+
+def test_rows_that_start_differently(nat):
+    """x, residual, sum and y each off a 16-byte boundary by another amount."""
+    g = gen(18)
+    for rows, cols in ((3, 700), (400, 1500)):
+        x, r, h, y = (torch.zeros(rows * cols + 8, device="cuda", dtype=torch.bfloat16)
+                      [o:o + rows * cols].view(rows, cols) for o in (0, 1, 3, 6))
+        x.copy_(randn(g, rows, cols))
+        r.copy_(randn(g, rows, cols))
+        nat.bv_rms_norm(x, None, residual=r, h=h, y=y)
+        check_norm(x, r, None, 1e-6, y, h)
+        q = torch.zeros(rows * cols + 8, device="cuda", dtype=torch.int8)[3:3 + rows * cols]
+        q = q.view(rows, cols)
+        nat.bv_quantize_rows(r, q=q)
+        np.testing.assert_array_equal(q.cpu().numpy(), expected_q(r, None, None)[0])
+
+
+def test_gains_that_start_anywhere(nat):
+    g = gen(19)
+    for dtype in ALL:
+        for cols in (1000, 1024, 1031):
+            gain = (1 + 0.3 * randn(g, cols + 3)).to(dtype)[3:]
+            for rows in (4, 400):
+                x = randn(g, rows, cols).to(dtype)
+                check_norm(x, None, gain, 1e-6, nat.bv_rms_norm(x, gain), None)
 
 
 def test_broadcast_rows_and_leading_dims(nat):
