@@ -210,8 +210,8 @@ struct Piece {
 // once, so the dot products stay on the CUDA cores (four products an
 // instruction) and nothing is staged.  A block takes R rows and all of K: a
 // thread reads 16 bytes of each row and column at a time, 128 threads apart.
-// One token x 8192 x 8192: 15.9 us = 4.2 TB/s; x 4096 x 4096 5.9 us, most of it
-// the launch and the first bytes' latency.
+// One token x 8192 x 8192: 14.3 us = 4.7 TB/s; x 4096 x 4096 4.8 us = 3.5 TB/s,
+// where the first bytes' latency counts.
 
 constexpr int DOT_THREADS = 128;
 
@@ -223,6 +223,8 @@ __global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p) {
   const int8_t *rhi = p.r + (int64_t)(p.rows - 1) * p.rstride + p.K;
   const int8_t *chi = p.c + (int64_t)(p.cols - 1) * p.cstride + p.K;
   int acc[R][C] = {};
+  admit_next();
+  after_previous();
   for (int k = 16 * threadIdx.x; k < p.K; k += 16 * DOT_THREADS) {
     uint4 r[R], c[C];
     if (ALIGNED && k + 16 <= p.K) {
@@ -292,7 +294,8 @@ __global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p) {
 // product, and only a split over K gives every SM some of them.  The shares
 // are joined through distributed shared memory: each CTA leaves its partial
 // sums in its own, then sums and writes NT / split of the columns.  Integers, so
-// the join's order does not show.  (Adding to the owner's shared memory from
+// the join's order does not show.  24 x 2048 x 8192: 9.3 us, 64 x 4096 x 4096 10.4 us =
+// 1.6 TB/s: set-up, the first bytes' latency and the join take most of it.  (Adding to the owner's shared memory from
 // afar instead took longer: 16 x 8192 x 2048 11.2 us, 10.0 us so.)
 //
 // Thread 0 loads the stages by TMA.  Where an operand's rows do not start on 16
@@ -357,6 +360,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
   const unsigned tmem = ctl.tmem;
+  admit_next();
+  after_previous();
   // what the epilogue needs of the scales, on its way during the products
   const int row = row0 + 32 * warp + lane;  // of warps 0..3
   const bool in = warp < 4 && row < p.rows;
@@ -544,10 +549,10 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
 // ring of stages, and two accumulators of NT columns in TMEM let sixteen warps a
 // CTA write one tile out while the tensor cores work on the next.  Tiles are
 // walked in bands of BAND row tiles, so that the pairs at work at one time share
-// operand tiles in L2.  8192 x 8192 x 8192: 369 us = 2.98 POP/s, the tensor pipe 84 %
+// operand tiles in L2.  8192 x 8192 x 8192: 357 us = 3.08 POP/s, the tensor pipe 84 %
 // busy at the 1.58 GHz that the power cap leaves it.  With a short K the operands'
-// way from L2 and the epilogue bound it: 4800 x 4096 x 1024 27.0 us (products alone
-// 21 us with eight epilogue warps, which took 31.7 us in all).
+// way from L2 and the epilogue bound it: 4800 x 4096 x 1024 24.9 us (with eight
+// epilogue warps, before launches overlapped, 31.7 us, its products alone 21 us).
 
 constexpr int PAIR_EPI_WARPS = 16;  // of a CTA: four for each 32 rows
 constexpr int PAIR_THREADS = 128 + 32 * PAIR_EPI_WARPS;
@@ -623,6 +628,8 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   cluster_sync();  // both CTAs' barriers exist before anyone signals them
   asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
   const unsigned tmem = ctl.tmem;
+  admit_next();
+  after_previous();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -802,18 +809,8 @@ bv_status run_tile(const Mm &p, int split, cudaStream_t st) {
   if (!COPY_C) BV_TRY(encode_rows(&mc, p.c, p.cstride, p.cols, p.K, NT));
   int *status = device_status_ptr();
   if (!status) return fail(BV_ERR_CUDA, "bv_int8_matmul: status word");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
-  cfg.blockDim = dim3(COPY_R || COPY_C ? 128 + 32 * COPY_WARPS : 128);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)split, 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, mr, mc, p, (int)tiles_r, split, stages, status,
-                              wait_limit()));
+  CUDA_TRY(launch_next(kernel, tiles * split, COPY_R || COPY_C ? 128 + 32 * COPY_WARPS : 128, smem,
+                       split, st, mr, mc, p, (int)tiles_r, split, stages, status, wait_limit()));
   return BV_OK;
 }
 
@@ -833,15 +830,15 @@ bv_status run_pair(const Mm &p, cudaStream_t st) {
   int *status = device_status_ptr();
   if (!status) return fail(BV_ERR_CUDA, "bv_int8_matmul: status word");
   const int grid = 2 * (int)std::min<int64_t>(tiles_r * tiles_c, 74);
-  kernel<<<grid, PAIR_THREADS, smem, st>>>(mr, mc, p, (int)tiles_r, (int)tiles_c, status,
-                                           wait_limit());
+  CUDA_TRY(launch_next(kernel, grid, PAIR_THREADS, smem, 1, st, mr, mc, p, (int)tiles_r, (int)tiles_c,
+                       status, wait_limit()));
   return BV_OK;
 }
 
 template <typename T, int R, int C, bool ALIGNED>
 bv_status run_dot(const Mm &p, cudaStream_t st) {
-  int8_dot_kernel<T, R, C, ALIGNED>
-      <<<(unsigned)((p.rows + (int64_t)R - 1) / R), DOT_THREADS, 0, st>>>(p);
+  CUDA_TRY(launch_next(int8_dot_kernel<T, R, C, ALIGNED>, (p.rows + (int64_t)R - 1) / R, DOT_THREADS, 0,
+                       1, st, p));
   return BV_OK;
 }
 template <typename T, int C, bool ALIGNED>

@@ -469,6 +469,8 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 128) rows_kernel(NormArgs a, in
   const T *x0 = static_cast<const T *>(a.x), *x1 = x0 + (a.rows - 1) * a.xs + a.cols;
   const T *r0 = static_cast<const T *>(a.residual), *r1 = r0 + (a.rows - 1) * a.rs + a.cols;
   int buf = 0;
+  admit_next();
+  after_previous();
   for (int64_t first = blockIdx.x * (int64_t)per; first < a.rows; first += gridDim.x * (int64_t)per) {
     int64_t row = first + (BLOCK ? 0 : threadIdx.x / tpr);
     // lanes past the last row take part in the warp's steps with no columns
@@ -558,10 +560,14 @@ stream_rows_kernel(NormArgs a, Ring ring, int *status, long long wait_limit) {
     fetch_row(x, xe, dst, bar, true);
     if (residual) fetch_row(r, re, dst + ring.row_bytes, bar, true);
   };
+  admit_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < ring.slots; ++s) mbar_init(full + 8 * s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+  }
+  after_previous();
+  if (threadIdx.x == 0) {
     for (int s = 0; s < ring.slots; ++s)
       if (blockIdx.x + s * step < a.rows) fetch(blockIdx.x + s * step, s);
   }
@@ -641,6 +647,8 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(NormArgs a) {
   int buf = 0;
   const G *gain = static_cast<const G *>(a.gain);
   const int n = blockDim.x;
+  admit_next();
+  after_previous();
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T *x = static_cast<const T *>(a.x) + row * a.xs;
     const T *r = static_cast<const T *>(a.residual) + row * a.rs;
@@ -720,7 +728,7 @@ bv_status launch_stream(const NormArgs &a, int threads, cudaStream_t st) {
   BV_TRY(ensure_dynamic_smem((const void *)k, smem + 2048, "rms_norm smem"));
   // (RAGGED: in eights, so that a block's rows all have the same m)
   const int64_t blocks = std::min<int64_t>(a.rows, RAGGED ? kSms * per_sm / 8 * 8 : kSms * per_sm);
-  k<<<(unsigned)blocks, threads, smem, st>>>(a, ring, status, wait_limit());
+  CUDA_TRY(launch_next(k, blocks, threads, smem, 1, st, a, ring, status, wait_limit()));
   return BV_OK;
 }
 
@@ -728,8 +736,8 @@ template <typename T, typename G, int NV, bool BLOCK, Mode MODE, bool RAGGED>
 bv_status launch_direct(const NormArgs &a, int threads, cudaStream_t st) {
   const int per = BLOCK ? 1 : 128 / threads;
   const int64_t blocks = std::min<int64_t>((a.rows + per - 1) / per, 0x7fffffff);
-  rows_kernel<T, G, NV, BLOCK, MODE, RAGGED>
-      <<<(unsigned)blocks, BLOCK ? threads : 128, 0, st>>>(a, threads);
+  CUDA_TRY(launch_next(rows_kernel<T, G, NV, BLOCK, MODE, RAGGED>, blocks, BLOCK ? threads : 128, 0,
+                       1, st, a, threads));
   return BV_OK;
 }
 
@@ -786,8 +794,9 @@ bv_status launch_typed(const NormArgs &a, cudaStream_t st) {
     return launch_vec<T, G, MODE, false>(a, st);
   if (fits && follows(a.residual, a.rs) && follows(a.sum, a.ss) && follows(a.y, a.ys))
     return launch_vec<T, G, MODE, true>(a, st);
-  const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 0x7fffffff);
-  long_rows_kernel<T, G, MODE><<<grid, std::min(1024, up32((a.cols + 3) / 4)), 0, st>>>(a);
+  const int64_t grid = std::min<int64_t>(a.rows, 0x7fffffff);
+  const int threads = a.cols >= 4096 ? 1024 : up32((a.cols + 3) / 4);
+  CUDA_TRY(launch_next(long_rows_kernel<T, G, MODE>, grid, threads, 0, 1, st, a));
   return BV_OK;
 }
 

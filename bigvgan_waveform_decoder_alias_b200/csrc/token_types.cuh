@@ -3,6 +3,8 @@
 
 #include <cuda_bf16.h>
 
+#include <utility>
+
 #include "common.cuh"
 
 namespace bv {
@@ -97,6 +99,43 @@ __device__ __forceinline__ uint4 bytes_from(const uint4 &a, const uint4 &b, int 
   const int s = 8 * (off & 3);
   return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
                     __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+}
+
+// The token operators follow one another in short launches, so each may be
+// scheduled before the kernel ahead of it has ended (launch_next): its blocks
+// set up and then wait (after_previous) until that kernel has completed and its
+// writes are visible.  Nothing in memory is touched before.  A kernel lets the
+// next one in (admit_next) when all its blocks hold what they need of an SM,
+// TMEM too: the next one's blocks, which wait for it, can then take nothing that
+// it still asks for.  (Launches back to back: the norm of one row of 4096 bf16
+// values 2.5 -> 2.05 us, a product of 24 x 2048 x 8192 11.1 -> 9.3 us.  The
+// figures beside the rules that choose kernels and tiles were taken before,
+// on both sides alike.)
+__device__ __forceinline__ void admit_next() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cluster,
+                        cudaStream_t st, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 // ---- launchers (arguments checked by the ABI entries) ------------------------
