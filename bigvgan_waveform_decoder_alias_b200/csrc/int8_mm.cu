@@ -796,7 +796,10 @@ bv_status run_tile(const Mm &p, int split, cudaStream_t st) {
   if (tiles * split > 0x7fffffff) return fail(BV_ERR_SHAPE, "bv_int8_matmul: grid");
   constexpr int STAGE = tile_stage_bytes<NT>();
   const int per = (chunks + split - 1) / split;
-  // two CTAs an SM; room for the partial sums of a split tile
+  // Two CTAs an SM; room for the partial sums of a split tile.  A CTA of a split
+  // tile has two stages at least (per >= 2), so that the TMEM of such CTAs fits an
+  // SM whose shared memory they fit: one that waited for TMEM would hold up its
+  // cluster.
   int stages = std::min(std::min(per, TILE_MAX_STAGES), (112 * 1024 - 1024) / STAGE);
   const int least = split > 1 ? (NT * BR * 4 + STAGE - 1) / STAGE : 1;
   stages = std::max(stages, least);
