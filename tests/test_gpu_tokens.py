@@ -464,6 +464,75 @@ def test_streams_and_two_calls_at_once(nat):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (40, 300, 4096), (700, 1024, 1001), (600, 4096, 512)])
+def test_launches_keep_their_order(nat, M, N, K):
+    """Kernels that may be scheduled early still read what the one before them
+    wrote, and overwrite nothing it reads: a chain over the same few buffers,
+    with other kernels between, against the same chain with a wait after each
+    step."""
+    g = gen(20)
+    w, sw = nat.bv_quantize_rows(randn(g, N, K))
+    back, sb = nat.bv_quantize_rows(randn(g, K, N))
+    start = randn(g, M, K)
+
+    def chain(wait):
+        def step(r):
+            if wait:
+                torch.cuda.synchronize()
+            return r
+        x = start.clone()
+        total = torch.zeros_like(x)
+        q = torch.empty(M, (K + 15) // 16 * 16, device="cuda", dtype=torch.int8)[:, :K]
+        p = torch.empty(M, (N + 15) // 16 * 16, device="cuda", dtype=torch.int8)[:, :N]
+        s, sp = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        y, z = torch.empty(M, N, device="cuda"), torch.empty(M, K, device="cuda")
+        for i in range(40):
+            step(nat.bv_rms_norm_int8(x, None, residual=start, h=x, q=q, scale=s))
+            step(nat.bv_int8_matmul(q, s, w, sw, y=y))
+            step(nat.bv_quantize_rows(y, q=p, scale=sp))
+            step(nat.bv_int8_matmul(p, sp, back, sb, residual=x, y=z))
+            step(nat.bv_rms_norm(z, None, y=x))
+            if i % 3 == 0:
+                step(total.add_(x))
+                step(z.zero_())
+        return total
+    want = chain(True)
+    assert torch.isfinite(want).all()
+    for _ in range(3):
+        assert torch.equal(chain(False), want)
+
+
+@pytest.mark.parametrize("rows", [3, 500])
+def test_calls_wait_for_events_of_other_streams(nat, rows):
+    """A call behind an event waits for what the event stands for, although a
+    kernel of the same kind ran just before it on its own stream."""
+    g = gen(21)
+    big = randn(g, 4096, 4096)
+    other = randn(g, rows, 1024)
+    w, sw = nat.bv_quantize_rows(randn(g, 64, 1024))
+    x = torch.zeros(rows, 1024, device="cuda")
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for i in range(8):
+        x.zero_()
+        fresh = randn(g, rows, 1024)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            for _ in range(3):
+                big @ big  # keeps s1 busy for milliseconds
+            x.copy_(fresh)
+            ready = torch.cuda.Event()
+            ready.record(s1)
+        with torch.cuda.stream(s2):
+            nat.bv_rms_norm(other)
+            s2.wait_event(ready)
+            q, s = nat.bv_rms_norm_int8(x)
+            y = nat.bv_int8_matmul(q, s, w, sw)
+        torch.cuda.synchronize()
+        q1, s1_ = nat.bv_rms_norm_int8(fresh)
+        assert torch.equal(q, q1) and torch.equal(s, s1_)
+        assert torch.equal(y, nat.bv_int8_matmul(q1, s1_, w, sw))
+
+
 def test_captured_and_replayed(nat):
     """Two graphs of the same layer, replayed in turn on new inputs."""
     g = gen(12)
