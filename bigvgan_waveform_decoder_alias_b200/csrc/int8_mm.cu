@@ -182,13 +182,13 @@ struct Piece {
     const bool two = at + n > 16;
     if (w >= lo && w + (two ? 32 : 16) <= hi) {
       off = at;
-      a = __ldg(reinterpret_cast<const uint4 *>(w));
-      if (two) b = __ldg(reinterpret_cast<const uint4 *>(w) + 1);
+      a = *reinterpret_cast<const uint4 *>(w);
+      if (two) b = reinterpret_cast<const uint4 *>(w)[1];
     } else {
       unsigned v[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (i < n) v[i / 4] |= (unsigned)(uint8_t)__ldg(p + i) << (8 * (i % 4));
+        if (i < n) v[i / 4] |= (unsigned)(uint8_t)p[i] << (8 * (i % 4));
       a = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
@@ -230,12 +230,12 @@ __global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p) {
     if (ALIGNED && k + 16 <= p.K) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        r[i] = __ldg(reinterpret_cast<const uint4 *>(
-            p.r + (int64_t)min(row0 + i, p.rows - 1) * p.rstride + k));
+        r[i] = *reinterpret_cast<const uint4 *>(
+            p.r + (int64_t)min(row0 + i, p.rows - 1) * p.rstride + k);
 #pragma unroll
       for (int j = 0; j < C; ++j)
-        c[j] = __ldg(reinterpret_cast<const uint4 *>(
-            p.c + (int64_t)min(j, p.cols - 1) * p.cstride + k));
+        c[j] = *reinterpret_cast<const uint4 *>(
+            p.c + (int64_t)min(j, p.cols - 1) * p.cstride + k);
     } else {
       Piece pr[R], pc[C];
 #pragma unroll
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(DOT_THREADS) int8_dot_kernel(const Mm p) {
   const bool mine = threadIdx.x < R * C && row < p.rows && j < p.cols;
   float s = 0.0f, b = 0.0f, res = 0.0f;
   if (mine) {
-    s = __fmul_rn(__ldg(p.c_scale + j), __ldg(p.r_scale + row));
-    b = p.r_bias ? __ldg(p.r_bias + row) : p.c_bias ? __ldg(p.c_bias + j) : 0.0f;
+    s = __fmul_rn(p.c_scale[j], p.r_scale[row]);
+    b = p.r_bias ? p.r_bias[row] : p.c_bias ? p.c_bias[j] : 0.0f;
     if (p.residual) res = to_f32(static_cast<const T *>(p.residual)[j * p.rs + row]);
   }
   __syncthreads();
@@ -365,13 +365,13 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
   // what the epilogue needs of the scales, on its way during the products
   const int row = row0 + 32 * warp + lane;  // of warps 0..3
   const bool in = warp < 4 && row < p.rows;
-  const float rscale = in ? __ldg(p.r_scale + row) : 0.0f;
-  const float rbias = in && p.r_bias ? __ldg(p.r_bias + row) : 0.0f;
+  const float rscale = in ? p.r_scale[row] : 0.0f;
+  const float rbias = in && p.r_bias ? p.r_bias[row] : 0.0f;
   if (warp == 2 || warp == 3)
     for (int c = threadIdx.x - 64; c < NT; c += 64) {
       const bool have = col0 + c < p.cols;
-      cs[c] = have ? __ldg(p.c_scale + col0 + c) : 0.0f;
-      cb[c] = have && p.c_bias ? __ldg(p.c_bias + col0 + c) : 0.0f;
+      cs[c] = have ? p.c_scale[col0 + c] : 0.0f;
+      cb[c] = have && p.c_bias ? p.c_bias[col0 + c] : 0.0f;
     }
 
   if (TMA && warp == 0 && lane == 0) {
@@ -443,8 +443,8 @@ int8_tile_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
             if (g + i >= PASSES) continue;
             const int8_t *w = from[g + i] + k;
             w -= reinterpret_cast<uintptr_t>(w) & 15;
-            lo[i] = __ldg(reinterpret_cast<const uint4 *>(w));
-            hi[i] = __ldg(reinterpret_cast<const uint4 *>(w) + 1);
+            lo[i] = *reinterpret_cast<const uint4 *>(w);
+            hi[i] = reinterpret_cast<const uint4 *>(w)[1];
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -712,11 +712,11 @@ int8_pair_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constan
       int row0, col0;
       tile_at(tau, row0, col0);
       const int row = row0 + 32 * q + lane, col = col0 + ct;
-      n_rs = row < p.rows ? __ldg(p.r_scale + row) : 0.0f;
-      n_rb = row < p.rows && p.r_bias ? __ldg(p.r_bias + row) : 0.0f;
+      n_rs = row < p.rows ? p.r_scale[row] : 0.0f;
+      n_rb = row < p.rows && p.r_bias ? p.r_bias[row] : 0.0f;
       const bool have = ct < NT && col < p.cols;
-      n_cs = have ? __ldg(p.c_scale + col) : 0.0f;
-      n_cb = have && p.c_bias ? __ldg(p.c_bias + col) : 0.0f;
+      n_cs = have ? p.c_scale[col] : 0.0f;
+      n_cb = have && p.c_bias ? p.c_bias[col] : 0.0f;
     };
     fetch(pid);
     int it = 0;

@@ -279,19 +279,19 @@ __device__ __forceinline__ Pack<G, VEC> load_gain(const G *gain, const Lay<VEC, 
       const char *w = p - off;
       if (l.whole(i) && w >= reinterpret_cast<const char *>(gain) &&
           w + 32 <= reinterpret_cast<const char *>(gain + l.cols)) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(w));
-        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w) + 1);
+        const uint4 a = *reinterpret_cast<const uint4 *>(w);
+        const uint4 b = reinterpret_cast<const uint4 *>(w)[1];
         *reinterpret_cast<uint4 *>(&g) = bytes_from(a, b, off);
         return g;
       }
     } else if (l.whole(i)) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) g.v[e] = __ldg(gain + first + e);
+      for (int e = 0; e < VEC; ++e) g.v[e] = gain[first + e];
       return g;
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-      g.v[e] = l.has(i, e) ? __ldg(gain + first + e) : from_f32<G>(0.0f);
+      g.v[e] = l.has(i, e) ? gain[first + e] : from_f32<G>(0.0f);
     return g;
   }
 }

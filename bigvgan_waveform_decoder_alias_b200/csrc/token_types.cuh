@@ -104,7 +104,10 @@ __device__ __forceinline__ uint4 bytes_from(const uint4 &a, const uint4 &b, int 
 // The token operators follow one another in short launches, so each may be
 // scheduled before the kernel ahead of it has ended (launch_next): its blocks
 // set up and then wait (after_previous) until that kernel has completed and its
-// writes are visible.  Nothing in memory is touched before.  A kernel lets the
+// writes are visible.  Nothing in memory is touched before, and what is read
+// after is read by plain loads or copies: the read-only path (__ldg) is for data
+// that nobody writes while the kernel runs, and the kernel ahead may still write
+// these operands when this one has begun.  A kernel lets the
 // next one in (admit_next) when all its blocks hold what they need of an SM,
 // TMEM too: the next one's blocks, which wait for it, can then take nothing that
 // it still asks for.  (Launches back to back: the norm of one row of 4096 bf16

@@ -164,3 +164,18 @@ def test_python_wrappers_refuse_host_tensors(L):
         native.bv_int8_matmul(q, s, q, s)
     with pytest.raises(native.BVError):
         native.bv_int8_matmul(x, s, q, s)
+
+
+@pytest.mark.parametrize("name", ["rows.cu", "int8_mm.cu"])
+def test_overlapped_kernels_read_by_plain_loads(name):
+    """Kernels that begin before the one ahead of them has ended may not read
+    through the read-only path, whose data no one may write meanwhile: a product
+    reads the 8-bit rows and scales that the norm ahead of it writes."""
+    import os
+    import re
+
+    from bigvgan_waveform_decoder_alias_b200 import build_native
+    text = open(os.path.join(build_native.CSRC, name)).read()
+    assert "after_previous()" in text  # launched ahead of time
+    code = re.sub(r"//[^\n]*", "", text)
+    assert not re.search(r"__ldg\s*\(|ld\.global\.nc|__restrict__", code)
