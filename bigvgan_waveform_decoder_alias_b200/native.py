@@ -808,7 +808,9 @@ def bv_int8_matmul(a, a_scale, w, w_scale, bias=None, residual=None, out_dtype=N
 class TokenFrontEnd:
     """A model's last norm and its projection into latents, in 8 bits: gain
     [cols] or None, weight [Cout, cols] (quantised here, one scale a channel),
-    bias [Cout] or None."""
+    bias [Cout] or None.  Made on the current stream, which is waited for, so it
+    may be called at once on any stream (made inside a graph's capture, its
+    weight is there once the graph has run)."""
 
     def __init__(self, gain, weight, bias=None, eps=1e-6, device="cuda"):
         weight = torch.as_tensor(weight).to(device).contiguous()
@@ -822,6 +824,10 @@ class TokenFrontEnd:
         self.bias = None if bias is None else \
             torch.as_tensor(bias, dtype=torch.float32).to(device).contiguous()
         self.eps = eps
+        if self.w.is_cuda:
+            with torch.cuda.device(self.w.device):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
 
     def __call__(self, x, residual=None, by_side=False, z=None, workspace=None, stream=None):
         """x [S, T, cols] (+ residual) -> latents [Cout, S, T], or [S, Cout, T]

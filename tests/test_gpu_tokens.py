@@ -750,3 +750,23 @@ def test_bounded_waits_report_and_leave_the_context_usable(nat, call):
         check_norm(x, None, None, 1e-6, y, None)
     else:
         check_product(a, sa, w, sw, None, None, y, torch.float32, False)
+
+
+def test_front_end_is_called_at_once_on_another_stream(nat):
+    """Made behind queued work on one stream and called on another without a
+    wait between: the call reads the finished weight."""
+    g = gen(22)
+    big = randn(g, 4096, 4096)
+    x = randn(g, 2, 30, 256)
+    other = torch.cuda.Stream()
+    for _ in range(6):
+        weight = randn(g, 32, 256)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            big @ big  # keeps the current stream busy for milliseconds
+        front = nat.TokenFrontEnd(None, weight)
+        z = front(x, stream=other)
+        other.synchronize()
+        q, s = nat.bv_quantize_rows(weight)
+        assert torch.equal(front.w, q) and torch.equal(front.w_scale, s)
+        assert torch.equal(z, front(x))

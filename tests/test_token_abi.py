@@ -179,3 +179,27 @@ def test_overlapped_kernels_read_by_plain_loads(name):
     assert "after_previous()" in text  # launched ahead of time
     code = re.sub(r"//[^\n]*", "", text)
     assert not re.search(r"__ldg\s*\(|ld\.global\.nc|__restrict__", code)
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_front_end_waits_for_its_weight(L, monkeypatch, capturing):
+    """A front end quantises its weight on the stream it is made on and may then
+    be called on any other: its constructor waits for that stream (but not in a
+    capture, where a wait is an error)."""
+    from contextlib import nullcontext
+    from types import SimpleNamespace
+
+    from bigvgan_waveform_decoder_alias_b200 import native
+    steps = []
+    q = SimpleNamespace(is_cuda=True, device="cuda:0")
+
+    def quantise(x):
+        steps.append("quantise")
+        return q, q
+    monkeypatch.setattr(native, "bv_quantize_rows", quantise)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: SimpleNamespace(
+        synchronize=lambda: steps.append("wait")))
+    native.TokenFrontEnd(None, torch.zeros(4, 8), device="cpu")
+    assert steps == (["quantise"] if capturing else ["quantise", "wait"])
