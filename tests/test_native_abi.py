@@ -184,3 +184,51 @@ def test_weights_from_flat_walks_module_order(nat):
     assert a.conv1_w[1] == offs["stage1.block2.unit1.conv1.w"]
     assert a.act_log_beta[3] == offs["stage1.block2.unit1.act2.log_beta"]
     assert w.post_w == offs["conv_post.w"] and w.post_b == offs["conv_post.b"]
+
+
+def test_tensor_map_encoder_is_looked_up_once_for_all_threads(tmp_path):
+    """Threads that make their first call together all get the driver's tensor
+    map encoder, although looking it up takes a while (a stand-in that takes 0.2 s
+    here; the lookup is host code, no device is involved)."""
+    import shutil
+    import subprocess
+
+    from bigvgan_waveform_decoder_alias_b200 import build_native
+    src = tmp_path / "encoder.cu"
+    src.write_text(r"""
+#include <atomic>
+#include <chrono>
+#include <thread>
+#include <vector>
+#include "tc_ptx.cuh"
+static std::atomic<int> lookups{0}, started{0};
+static int target;
+extern "C" cudaError_t CUDARTAPI cudaGetDriverEntryPoint(const char *, void **p, unsigned long long,
+                                                         cudaDriverEntryPointQueryResult *q) {
+  ++lookups;
+  std::this_thread::sleep_for(std::chrono::milliseconds(200));
+  *p = &target;
+  *q = cudaDriverEntryPointSuccess;
+  return cudaSuccess;
+}
+int main() {
+  std::atomic<int> missing{0};
+  std::vector<std::thread> threads;
+  for (int i = 0; i < 8; ++i)
+    threads.emplace_back([&] {
+      ++started;
+      while (started < 8) {}
+      if (reinterpret_cast<void *>(bv::encode_fn()) != &target) ++missing;
+    });
+  for (auto &t : threads) t.join();
+  std::printf("missing %d lookups %d\n", missing.load(), lookups.load());
+  return 0;
+}
+""")
+    exe = tmp_path / "encoder"
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    flags = [f for f in build_native.NVCC_FLAGS if f not in ("-shared", "-lineinfo")]
+    subprocess.check_call([nvcc, *flags, "-cudart", "shared", "-I", build_native.INCLUDE, "-I",
+                           build_native.CSRC, "-o", str(exe), str(src)])
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert out.stdout == "missing 0 lookups 1\n", out.stdout + out.stderr
