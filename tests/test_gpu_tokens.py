@@ -770,3 +770,32 @@ def test_front_end_is_called_at_once_on_another_stream(nat):
         q, s = nat.bv_quantize_rows(weight)
         assert torch.equal(front.w, q) and torch.equal(front.w_scale, s)
         assert torch.equal(z, front(x))
+
+
+@pytest.mark.parametrize("short", [1, 500])
+def test_the_longest_rows(nat, short):
+    """A row of 2^31 - short values: neither the count of its groups nor the
+    step past its end may leave 32 bits.  Whole numbers up to 127, so q is x."""
+    cols, step = 2 ** 31 - short, 1 << 26
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    x = torch.empty(1, cols, device="cuda", dtype=torch.bfloat16)
+    squares = 0.0
+    for at in range(0, cols, step):
+        i = torch.arange(at, min(at + step, cols), device="cuda")
+        v = ((i * 2654435761) >> 7) % 255 - 127
+        x[0, at:at + step] = v
+        squares += float((v * v).sum())
+    q, scale = nat.bv_quantize_rows(x)
+    assert float(scale) == 1.0
+    for at in range(0, cols, step):
+        assert torch.equal(q[0, at:at + step], x[0, at:at + step].to(torch.int8)), at
+    del q
+    y, h = nat.bv_rms_norm(x, residual=x)
+    rstd = (4 * squares / cols + 1e-6) ** -0.5
+    rel = (CHAIN(cols) / 2 + 8) * U + HALF[torch.bfloat16]
+    for at in range(0, cols, step):
+        part = x[0, at:at + step].float()
+        assert torch.equal(h[0, at:at + step].float(), 2 * part), at
+        want = 2 * part * rstd
+        assert bool(((y[0, at:at + step].float() - want).abs() <= want.abs() * rel * 1.001).all()), at
