@@ -642,8 +642,10 @@ stream_rows_kernel(NormArgs a, Ring ring, int *status, long long wait_limit) {
 // from L2).  The sum is written on the second read, by the thread that read its
 // operands, so it may be x or the residual.  A row is walked in parts of
 // kPart values a thread, so that offsets within a part fit an int (with the
-// simple addresses that gives) however long the row is: 300 x 100000 bf16 values
-// 113 us, 40 x 40000 with a residual to 8 bits 25.2 us.
+// simple addresses that gives) however long the row is; a part's sum of squares
+// joins the thread's in 64 bits (of 2^26 equal values, 2^16 a thread, sums in 32
+// bits alone put y off by 1e-4 to 4e-4).  300 x 100000 bf16 values
+// 113 us, 40 x 40000 with a residual to 8 bits 24.5 us.
 constexpr int kPart = 64;
 template <typename T, typename G, Mode MODE>
 __global__ void __launch_bounds__(1024) long_rows_kernel(NormArgs a) {
@@ -666,17 +668,21 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(NormArgs a) {
     auto t_of = [&](float h, const G *g, int c) {
       return MODE != kQuant && a.gain ? __fmul_rn(h, to_f32(g[c])) : h;
     };
-    float s = 0.0f, top = 0.0f, hm = 0.0f;
+    double total = 0.0;
+    float top = 0.0f, hm = 0.0f;
     for (int64_t at = threadIdx.x; at < a.cols; at += step) {
       const int end = (int)min(step, a.cols - at);
+      float part = 0.0f;
 #pragma unroll 4
       for (int c = 0; c < end; c += n) {
         const float h = h_of(x + at, r + at, c);
-        s = fmaf(h, h, s);
+        part = fmaf(h, h, part);
         hm = max_abs(hm, h, 0.0f);
         top = max_abs(top, t_of(h, g + at, c), 0.0f);
       }
+      total += part;
     }
+    float s = (float)total;
     reduce_row<true>(s, top, red, buf, n);
     float rstd = 1.0f;
     if (MODE != kQuant) {
@@ -686,14 +692,17 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(NormArgs a) {
         reduce_row<true>(zero, hm, red, buf, n);
         if (hm < __uint_as_float(kInfBits)) {
           const float down = pow2(167 - (int)(__float_as_uint(hm) >> 23));
-          float d = 0.0f;
+          total = 0.0;
           for (int64_t at = threadIdx.x; at < a.cols; at += step) {
             const int end = (int)min(step, a.cols - at);
+            float part = 0.0f;
             for (int c = 0; c < end; c += n) {
               const float h = h_of(x + at, r + at, c) * down;
-              d = fmaf(h, h, d);
+              part = fmaf(h, h, part);
             }
+            total += part;
           }
+          float d = (float)total;
           reduce_row<true>(d, none, red, buf, n);
           rstd = row_rstd(d, a.cols, a.eps * down * down) * down;
         }

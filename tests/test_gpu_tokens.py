@@ -799,3 +799,19 @@ def test_the_longest_rows(nat, short):
         assert torch.equal(h[0, at:at + step].float(), 2 * part), at
         want = 2 * part * rstd
         assert bool(((y[0, at:at + step].float() - want).abs() <= want.abs() * rel * 1.001).all()), at
+
+
+@pytest.mark.parametrize("lift", [1.0, 1e20])
+def test_sum_of_many_equal_squares(nat, lift):
+    """2^16 values of a row to each thread: the sum of so many squares in 32 bits
+    would lose a part of each.  (Those of the lifted row are past 32 bits.)"""
+    cols = 1 << 26
+    x = torch.full((1, cols), 1.14 * lift, device="cuda")
+    y = nat.bv_rms_norm(x, eps=1e-6)
+    want = 1.0 / (1.0 + 1e-6 / float(x[0, 0]) ** 2) ** 0.5
+    # a part's 64 sums, the joint sum in 64 bits and its rounding, 10 sums over the
+    # block, halved by the root; division, eps, root and product
+    close(y, torch.full_like(y, want).double(), torch.full_like(y, want).double() * (75 / 2 + 8) * U)
+    q, scale = nat.bv_rms_norm_int8(x, eps=1e-6)
+    assert bool((q == 127).all())
+    assert abs(float(scale) * 127 / want - 1) <= (75 / 2 + 10) * U
