@@ -981,10 +981,12 @@ bv_status bv_int8_matmul(const int8_t *a, int64_t a_stride, const float *a_scale
   constexpr int kMaxRows = 0x7fffff00;  // tile indexes stay inside 32 bits
   if (M < 0 || M > kMaxRows || N < 1 || N > kMaxRows || K < 1 || K > BV_INT8_MAX_DEPTH)
     return fail(BV_ERR_SHAPE, "%s: M=%d N=%d K=%d", what, M, N, K);
-  const int64_t max_stride = (int64_t)1 << 28;  // rows (below 2^31) x stride x 4 bytes < 2^62
+  const int64_t max_stride = (int64_t)1 << 28, max_out = (int64_t)1 << 31;
+  const int64_t yr = channels_first ? N : M, yc = channels_first ? M : N;
   if (a_stride < 0 || a_stride > max_stride || w_stride < 0 || w_stride > max_stride ||
-      (residual && (residual_stride < 0 || residual_stride > (int64_t)1 << 31)) || y_stride < 0 ||
-      y_stride > (int64_t)1 << 31)
+      (residual && (residual_stride < 0 || residual_stride > max_out ||
+                    !extent_ok(yr, residual_stride, yc))) ||
+      y_stride < 0 || y_stride > max_out || !extent_ok(yr, y_stride, yc))
     return fail(BV_ERR_SHAPE, "%s: row stride", what);
   if (M == 0) return BV_OK;
   if (!a || !a_scale || !w || !w_scale || !y) return fail(BV_ERR_ARG, "%s: null pointer", what);
@@ -992,7 +994,6 @@ bv_status bv_int8_matmul(const int8_t *a, int64_t a_stride, const float *a_scale
   if (!aligned_to(a_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(bias, 4) ||
       !aligned_to(residual, es) || !aligned_to(y, es))
     return fail(BV_ERR_ARG, "%s: misaligned pointer", what);
-  const int64_t yr = channels_first ? N : M, yc = channels_first ? M : N;
   if (yr > 1 && y_stride < yc) return fail(BV_ERR_SHAPE, "%s: the rows of y overlap", what);
   const RowView vy{y, yr, y_stride * es, yc * es};
   const RowView vr{residual, yr, residual_stride * es, yc * es};

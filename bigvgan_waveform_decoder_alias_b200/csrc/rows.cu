@@ -835,11 +835,6 @@ bv_status launch_norm(const NormArgs &a, cudaStream_t st) {
   return a.q ? launch_typed<T, G, kNorm8>(a, st) : launch_typed<T, G, kNorm>(a, st);
 }
 
-// Row offsets of a tensor stay far inside 64 bits.
-bool extent_ok(int64_t rows, int64_t stride, int64_t cols) {
-  return ((double)rows * (double)stride + (double)cols) * 4.0 < 0x1p60;
-}
-
 // Views of a call's rows, for the overlap checks.
 RowView view(const void *p, int64_t rows, int cols, int64_t stride, int esize) {
   return RowView{p, rows, stride * esize, (int64_t)cols * esize};

@@ -12,6 +12,11 @@ namespace bv {
 inline bool dtype_ok(int dt) { return dt == BV_F32 || dt == BV_BF16 || dt == BV_F16; }
 inline int dtype_size(int dt) { return dt == BV_F32 ? 4 : 2; }
 
+// Row offsets of a tensor stay far inside 64 bits.
+inline bool extent_ok(int64_t rows, int64_t stride, int64_t cols) {
+  return ((double)rows * (double)stride + (double)cols) * 4.0 < 0x1p60;
+}
+
 // `rows` rows of `row_bytes` bytes, `stride` bytes apart.
 struct RowView {
   const void *p;

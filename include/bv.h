@@ -658,7 +658,8 @@ bv_status bv_quantize_rows(const void *x, int64_t x_stride, int64_t rows,
  * bv_decode reads).  K up to BV_INT8_MAX_DEPTH.  Rows of a and w that start
  * on 16 bytes (aligned pointer, stride a multiple of 16) are read fastest.
  * Errors: BV_ERR_ARG (null, misaligned or overlapping pointer, bad type),
- * BV_ERR_SHAPE (M < 0, N < 1, K out of range, strides). */
+ * BV_ERR_SHAPE (M < 0, N < 1, K out of range, a stride of a or w past 2^28 or
+ * of y or the residual past 2^31, a tensor of 2^58 elements). */
 #define BV_INT8_MAX_DEPTH 131071
 bv_status bv_int8_matmul(const int8_t *a, int64_t a_stride,
                          const float *a_scale, const int8_t *w,

@@ -203,3 +203,16 @@ def test_front_end_waits_for_its_weight(L, monkeypatch, capturing):
         synchronize=lambda: steps.append("wait")))
     native.TokenFrontEnd(None, torch.zeros(4, 8), device="cpu")
     assert steps == (["quantise"] if capturing else ["quantise", "wait"])
+
+
+@pytest.mark.parametrize("cf", [0, 1])
+def test_matmul_extents_stay_inside_64_bits(L, cf):
+    """Outputs and residuals of 2^62 values: their byte offsets would wrap, and
+    with them the overlap checks."""
+    far = dict(M=0x7fffff00, N=0x7fffff00, as_=0, ws=0, cf=cf, rs=0x7fffff00, ys=0x7fffff00,
+               a=1 << 20, w=1 << 21, sa=1 << 40, sw=1 << 42, bias=None, r=None)
+    assert matmul(L, **far) == SHAPE
+    assert matmul(L, **far | dict(M=64, N=64, ys=1 << 31, r=1 << 45, rs=1 << 32)) == SHAPE
+    # a broadcast residual has no extent of its own
+    if not torch.cuda.is_available():
+        assert matmul(L, rs=0) == CUDA
