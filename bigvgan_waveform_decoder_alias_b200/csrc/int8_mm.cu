@@ -978,8 +978,7 @@ bv_status bv_int8_matmul(const int8_t *a, int64_t a_stride, const float *a_scale
   const char *what = "bv_int8_matmul";
   clear_error();
   if (!dtype_ok(dtype)) return fail(BV_ERR_ARG, "%s: dtype %d", what, dtype);
-  constexpr int kMaxRows = 0x7fffff00;  // tile indexes stay inside 32 bits
-  if (M < 0 || M > kMaxRows || N < 1 || N > kMaxRows || K < 1 || K > BV_INT8_MAX_DEPTH)
+  if (M < 0 || M > kMaxMmRows || N < 1 || N > kMaxMmRows || K < 1 || K > BV_INT8_MAX_DEPTH)
     return fail(BV_ERR_SHAPE, "%s: M=%d N=%d K=%d", what, M, N, K);
   const int64_t max_stride = (int64_t)1 << 28, max_out = (int64_t)1 << 31;
   const int64_t yr = channels_first ? N : M, yc = channels_first ? M : N;

@@ -46,6 +46,11 @@ bv_status bv_token_front_end(const void *x, int64_t x_stride, const void *residu
       residual_stride > max_stride)) || w_stride < 0 || w_stride > max_stride)
     return fail(BV_ERR_SHAPE, "%s: row stride", what);
   const int64_t tokens = (int64_t)S * T;
+  // (what only the product would refuse is refused before the norm is launched)
+  if (Cout > kMaxMmRows || (by_side ? T : tokens) > kMaxMmRows || !extent_ok(tokens, Cout, 0))
+    return fail(BV_ERR_SHAPE, "%s: S=%d T=%d Cout=%d", what, S, T, Cout);
+  if (!aligned_to(w_scale, 4) || !aligned_to(bias, 4) || !aligned_to(z, 4))
+    return fail(BV_ERR_ARG, "%s: misaligned pointer", what);
   const int64_t xe = x_stride * (tokens - 1) + cols, re = residual_stride * (tokens - 1) + cols;
   const int es = dtype_ok(dtype) ? dtype_size(dtype) : 1;
   const RowView vws{workspace, 1, 0, (int64_t)need};
@@ -61,9 +66,6 @@ bv_status bv_token_front_end(const void *x, int64_t x_stride, const void *residu
     if (rows_overlap(vws, o)) return fail(BV_ERR_ARG, "%s: workspace overlaps a tensor", what);
     if (&o != &others[6] && rows_overlap(vz, o)) return fail(BV_ERR_ARG, "%s: z overlaps a tensor", what);
   }
-  // (what only the product would refuse is refused before the norm is launched)
-  if (!aligned_to(w_scale, 4) || !aligned_to(bias, 4) || !aligned_to(z, 4))
-    return fail(BV_ERR_ARG, "%s: misaligned pointer", what);
   int8_t *q = static_cast<int8_t *>(workspace);
   float *scale = reinterpret_cast<float *>(q + rows_bytes(tokens, cols));
   const int64_t qs = padded(cols);

@@ -170,6 +170,7 @@ struct Int8Args {
   int M, N, K;
   int channels_first;
 };
+constexpr int kMaxMmRows = 0x7fffff00;  // M and N: tile indexes stay inside 32 bits
 bv_status launch_int8_matmul(const Int8Args &a, int dtype, cudaStream_t st);
 
 }  // namespace bv

@@ -216,3 +216,14 @@ def test_matmul_extents_stay_inside_64_bits(L, cf):
     # a broadcast residual has no extent of its own
     if not torch.cuda.is_available():
         assert matmul(L, rs=0) == CUDA
+
+
+@pytest.mark.parametrize("kw", [
+    dict(S=1, T=0x7fffff80, Cout=1, by_side=0), dict(S=1, T=0x7fffff80, Cout=1, by_side=1),
+    dict(S=1, T=8, Cout=0x7fffff80), dict(S=1, T=0x7fffff00, Cout=0x7fffff00, ws=0)])
+def test_front_end_refuses_the_product_before_the_norm_runs(L, kw):
+    """Sizes that the product would refuse are refused before any launch (a call
+    that reached the norm would report the missing device here)."""
+    far = dict(xs=0, x=1 << 20, gain=None, w=1 << 21, sw=1 << 22, bias=None, z=1 << 40, wsp=1 << 50,
+               bytes=1 << 62, cols=16, ws=16)
+    assert front(L, **far | kw) == SHAPE
