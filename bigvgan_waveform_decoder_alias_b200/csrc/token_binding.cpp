@@ -266,6 +266,7 @@ void bind(const py::dict &at, const py::object &error) {
 }  // namespace
 
 PYBIND11_MODULE(_tokens, m) {
+  m.attr("built_for") = BUILT_FOR;  // the torch of the build, which the build script looks for
   m.def("bind", &bind);
   m.def("rms_norm", &rms_norm);
   m.def("rms_norm_int8", &rms_norm_int8);
