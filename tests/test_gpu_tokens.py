@@ -815,3 +815,78 @@ def test_sum_of_many_equal_squares(nat, lift):
     q, scale = nat.bv_rms_norm_int8(x, eps=1e-6)
     assert bool((q == 127).all())
     assert abs(float(scale) * 127 / want - 1) <= (75 / 2 + 10) * U
+
+
+# ------------------------------- products in many tiles, in place, in batches
+
+
+@pytest.mark.parametrize("cf", [False, True])
+@pytest.mark.parametrize("rows,cols,K", [
+    # rows (the dimension y keeps consecutive) x columns x depth, so many that a
+    # pair of CTAs works through five tiles of 256 rows and more, each with more
+    # steps of 128 than its ring of stages has slots: 256 columns a tile, ragged in
+    # every direction and in whole tiles, then 192, 128 and 64 columns
+    (4865, 4901, 1000), (5120, 4864, 1024), (33001, 571, 1000), (95500, 100, 1300),
+    (95499, 49, 1400)])
+def test_product_in_many_tiles(nat, rows, cols, K, cf):
+    M, N = (rows, cols) if cf else (cols, rows)
+    g = gen(rows + cols)
+    a, w = int8(g, M, K), int8(g, N, K)
+    sa, sw = (torch.rand(n, device="cuda", generator=g) * 0.01 + 1e-4 for n in (M, N))
+    bias = randn(g, N)
+    y = nat.bv_int8_matmul(a, sa, w, sw, bias=bias, channels_first=cf)
+    check_product(a, sa, w, sw, bias, None, y, torch.float32, cf)
+    sd = sw * (200.0 / K ** 0.5 / 73 ** 2)  # inside fp16's range
+    for dtype in (torch.bfloat16, torch.float16):
+        y = randn(g, *y.shape).to(dtype)
+        before = y.clone()
+        nat.bv_int8_matmul(a, sa, w, sd, bias=bias, residual=y, y=y, channels_first=cf)
+        check_product(a, sa, w, sd, bias, before, y, dtype, cf)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("cf", [False, True])
+@pytest.mark.parametrize("pad", [True, False])
+@pytest.mark.parametrize("rows,cols,K", [
+    (1001, 1, 600), (1000, 3, 601),            # dot products
+    (130, 301, 256), (1000, 200, 1003),        # tiles
+    (257, 20, 4100), (300, 60, 5000),          # tiles whose depth a cluster shares
+    (2002, 701, 500), (4000, 512, 640)])       # tiles of pairs
+def test_product_adds_in_place_everywhere(nat, rows, cols, K, pad, cf, dtype):
+    """The residual is y itself, each kernel, both layouts; with 16-bit types
+    whole words are written of which a neighbour read one half."""
+    M, N = (rows, cols) if cf else (cols, rows)
+    g = gen(rows + cols + K)
+    a, w = int8(g, M, K, pad), int8(g, N, K, pad)
+    sa, sw = (torch.rand(n, device="cuda", generator=g) * 0.01 + 1e-4 for n in (M, N))
+    sw = sw * (200.0 / K ** 0.5 / 73 ** 2)
+    y = randn(g, *((N, M) if cf else (M, N))).to(dtype)
+    before = y.clone()
+    assert nat.bv_int8_matmul(a, sa, w, sw, residual=y, y=y, channels_first=cf) is y
+    check_product(a, sa, w, sw, None, before, y, dtype, cf)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("cols", [1000, 1024, 5000])
+def test_tokens_in_batches_of_any_size(nat, dtype, cols):
+    """From 296 rows on rows go through another kernel, and a product of many
+    tokens through others: q and a product are the same bits, a row's scale and
+    norm the same to the roundings of their sums' orders."""
+    g = gen(cols)
+    x = randn(g, 2000, cols).to(dtype)
+    gain = 1 + 0.3 * randn(g, cols)
+    w, sw = nat.bv_quantize_rows(randn(g, 2100, cols))
+    bias = randn(g, 2100)
+    q, s = nat.bv_rms_norm_int8(x, gain)
+    y = nat.bv_rms_norm(x, gain)
+    z = nat.bv_int8_matmul(q, s, w, sw, bias=bias)
+    rel = 2 * (CHAIN(cols) / 2 + 10) * U  # each of the two off by half of it
+    for first, n in ((0, 1), (7, 3), (100, 40), (0, 295), (5, 296), (3, 1700)):
+        part = slice(first, first + n)
+        q1, s1 = nat.bv_rms_norm_int8(x[part], gain)
+        assert torch.equal(q1, q[part])
+        close(s1, s[part], s[part].double() * rel)
+        y1 = nat.bv_rms_norm(x[part], gain).double()
+        assert bool(((y1 - y[part].double()).abs() <=
+                     y1.abs() * (rel + 2 * HALF[dtype]) * 1.001 + TINY[dtype]).all())
+        assert torch.equal(nat.bv_int8_matmul(q[part], s[part], w, sw, bias=bias), z[part])
