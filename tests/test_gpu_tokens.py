@@ -890,3 +890,23 @@ def test_tokens_in_batches_of_any_size(nat, dtype, cols):
         assert bool(((y1 - y[part].double()).abs() <=
                      y1.abs() * (rel + 2 * HALF[dtype]) * 1.001 + TINY[dtype]).all())
         assert torch.equal(nat.bv_int8_matmul(q[part], s[part], w, sw, bias=bias), z[part])
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("T,D,C", [(30, 64, 32), (200, 1024, 32), (50, 1001, 64)])
+def test_front_end_against_the_unquantised_projection(nat, dtype, T, D, C):
+    """How far the 8 bits move the latents from norm and projection in 64 bits:
+    half a step (and its own 32-bit error) of every value of the rows and of the
+    weight, against the other's absolute values, and of both together."""
+    g = gen(T + D + C)
+    x = randn(g, 1, T, D).to(dtype)
+    gain, weight, bias = 1 + 0.2 * randn(g, D), randn(g, C, D) / D ** 0.5, randn(g, C)
+    z = nat.TokenFrontEnd(gain, weight, bias)(x)[:, 0].t().double()
+    y64 = norm64(x, None, gain, 1e-6)[2][0]
+    w64 = weight.double()
+    want = y64 @ w64.t() + bias.double()
+    rel = 127 * (CHAIN(D) / 2 + 10) * U + 1e-4
+    dy = y64.abs().amax(-1, keepdim=True) / 127 * (0.5 + rel)
+    dw = w64.abs().amax(-1, keepdim=True).t() / 127 * (0.5 + rel)
+    tol = y64.abs().sum(-1, keepdim=True) * dw + dy * w64.abs().sum(-1) + D * dy * dw
+    close(z, want, tol + (want.abs() + 1) * 100 * U)
