@@ -104,7 +104,9 @@ __device__ __forceinline__ void load_residual(const Mm &p, int row0, int lane, i
 // Those columns of the accumulator go out: `rscale`, `rbias` are this lane's
 // row's, cs and cb (shared memory, 8-byte aligned) the columns' scales and biases,
 // cb zeros where the bias belongs to the rows.  The residual (`r`) was loaded
-// before; it may be y, as each element is read by the thread that writes it.
+// before; it may be y: an element is read by the lane that writes it or, of the
+// 16-bit pairs below, by its neighbour, whose half of the word reaches the writer
+// through a shuffle after it was read.
 // A 16-bit column is half a word a lane, so lanes swap halves in pairs: the
 // even one writes two rows of the even column, the odd one two rows of the odd
 // column.
