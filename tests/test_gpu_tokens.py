@@ -910,3 +910,48 @@ def test_front_end_against_the_unquantised_projection(nat, dtype, T, D, C):
     dw = w64.abs().amax(-1, keepdim=True).t() / 127 * (0.5 + rel)
     tol = y64.abs().sum(-1, keepdim=True) * dw + dy * w64.abs().sum(-1) + D * dy * dw
     close(z, want, tol + (want.abs() + 1) * 100 * U)
+
+
+@pytest.mark.parametrize("rows", [3, 500])
+def test_captured_calls_wait_for_other_branches(nat, rows):
+    """A graph with two branches: a call behind the join reads what the other
+    branch wrote, although a kernel of the same kind is ahead of it on its own;
+    two such graphs replayed on two streams at once stay apart."""
+    g = gen(23)
+    big = randn(g, 2048, 2048)
+    w, sw = nat.bv_quantize_rows(randn(g, 64, 1024))
+    graphs, ins, outs = [], [], []
+    for i in range(2):
+        x, src, other = (torch.zeros(rows, 1024, device="cuda") for _ in range(3))
+        nat.bv_int8_matmul(*nat.bv_rms_norm_int8(x), w, sw)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                big @ big  # the other branch is the longer one
+                big @ big
+                x.copy_(src)
+            nat.bv_rms_norm(other)
+            main.wait_stream(side)
+            q, s = nat.bv_rms_norm_int8(x)
+            y = nat.bv_int8_matmul(q, s, w, sw)
+        graphs.append(graph)
+        ins.append((x, src))
+        outs.append((q, s, y))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(6):
+        for x, src in ins:
+            x.zero_()
+            src.copy_(randn(g, rows, 1024))
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, src), (q, s, y) in zip(ins, outs):
+            q1, s1 = nat.bv_rms_norm_int8(src)
+            assert torch.equal(q, q1) and torch.equal(s, s1)
+            assert torch.equal(y, nat.bv_int8_matmul(q1, s1, w, sw))
